@@ -47,7 +47,7 @@
  *     of time records the fact in the device error word and returns early; read it with
  *     ulysses_get_device_status(). The word holds (kernel << 24) | (role << 16) | site of the
  *     first wait that gave up: kernel 1 forward, 2 backward, 3 self-test, 4 projection
- *     GEMM; role 1 loads, 2 MMA issue, 3 softmax, 4 dQ reduction, 5 epilogue, 6 self-test.
+ *     GEMM, 5 paged attention; role 1 loads, 2 MMA issue, 3 softmax, 4 dQ reduction, 5 epilogue, 6 self-test.
  */
 #ifndef ULYSSES_H
 #define ULYSSES_H
@@ -265,6 +265,93 @@ int ulysses_usp_attn_bwd(ulysses_shape_t shape, int P_ring, const ulysses_mask_t
                          const void *q, const void *k, const void *v, const void *o, const float *lse,
                          const void *dO, void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
                          void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Serving from a paged key/value cache. A trained block answers requests whose keys and
+ * values live in pages of page_size tokens anywhere in a pool; a block table names each
+ * request's pages in order. Three calls make one step: ulysses_page_plan turns request
+ * lengths into block tables and slots, ulysses_kv_append writes the new tokens' keys and
+ * values to their slots, ulysses_paged_attn_fwd attends the new tokens over the pages. No
+ * length is read on the host, so a step can be captured into a graph and replayed while
+ * requests grow.
+ *
+ * Requests are packed without padding: with cu_q[B + 1] (int32, device) the row starts, request
+ * i owns rows [cu_q[i], cu_q[i+1]) of the T rows of q, k, v and o ([T][heads][d_h]); rows from
+ * cu_q[B] on belong to nobody and are left alone. kv_lens[i] (int32, device) counts the
+ * request's keys, its new tokens last. */
+
+/* The pool: K and V of token t of page p and key/value head h are the d_h consecutive bf16 at
+ *   k (or v) + p * page_stride + t * token_stride + h * head_stride   (strides in elements,
+ * positive multiples of 8; a stride of a dimension of one entry is not used). The token layout
+ * [num_pages][page_size][H_kv][d_h] and the head-major [num_pages][H_kv][page_size][d_h] are
+ * both of this form. page_size: a power of two from 16 to 4096; num_pages >= 1 and
+ * num_pages * page_size < 2^31 (a slot, page * page_size + token, is an int32). Pointers
+ * 16-byte aligned. */
+typedef struct {
+    void *k;
+    void *v;
+    int num_pages, page_size, H_kv, d_h;
+    int64_t page_stride, token_stride, head_stride;
+} ulysses_kv_cache_t;
+
+/* Block tables and slot maps of one step, from request lengths on the device. Request i holds
+ * c_i = cached_lens[i] tokens (clamped to [0, max_pages * page_size]) in the first
+ * ceil(c_i / page_size) entries of block_table[i][max_pages] (int32, rows table_stride elements
+ * apart) and adds new_lens[i] (negative counts as 0):
+ *   cu_q[0] = 0, cu_q[i+1] = min(T, sum_{j <= i} new_j): tokens past row T are dropped;
+ *   kv_lens[i] = c_i + cu_q[i+1] - cu_q[i];
+ *   new pages are taken from the end of the list free_pages[0 .. *n_free) (free_capacity entries
+ *   long) in request order: the x-th is free_pages[*n_free - 1 - x]. They are written to
+ *   block_table behind the request's pages; other entries keep their values. An entry for which
+ *   the list has no page (or none within [0, num_pages)) becomes -1;
+ *   slot_map[t] = page * page_size + offset of row t's token, or -1 where it has no page and
+ *   for rows from cu_q[B] to T;
+ *   info[0] = cu_q[B], info[1] = pages taken from the list, info[2] = pages that were wanted and
+ *   not there (list or table too short), info[3] = tokens dropped (int32, at most 2^31 - 1).
+ * The list itself and *n_free are read only: subtract info[1] from *n_free to keep the pages.
+ * Calling again with the same inputs gives the same outputs. B <= 8192 (else UNSUPPORTED);
+ * max_pages * page_size + T <= 2^31 - 1. No output may be one of the inputs. B = 0 or T = 0 are
+ * valid (cu_q[0] and info are still written). */
+int ulysses_page_plan(int B, int T, int page_size, int max_pages, int64_t table_stride, int num_pages,
+                      const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
+                      int free_capacity, const int32_t *n_free, int32_t *block_table, int32_t *cu_q,
+                      int32_t *kv_lens, int32_t *slot_map, int32_t *info, void *stream);
+
+/* Writes the keys and values of T new tokens to their slots: k, v [T][H_kv][d_h] bf16, rows
+ * k_stride and v_stride elements apart (multiples of 8, at least H_kv * d_h), 16-bit patterns moved
+ * unchanged. A token whose slot lies outside the pool (-1: padding, or no page) is skipped;
+ * everything else in the cache keeps its values. Slots should be distinct: where two tokens name
+ * the same one, each 16-byte piece of it holds one or the other. Any d_h that is a multiple of 8.
+ * k, v must not overlap the cache. */
+int ulysses_kv_append(const ulysses_kv_cache_t *cache, int T, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *slot_map, void *stream);
+
+/* Attention of the new tokens over the pages: row t of request i (n_i = cu_q[i+1] - cu_q[i] rows)
+ * has position p = kv_lens[i] - n_i + t, and
+ *   S = softmax_scale * q k^T,  o = softmax(S) v,  lse = ln sum exp(S)
+ * over the request's permitted keys s: 0 <= s < kv_lens[i], with page block_table[i][s / page_size]
+ * inside the pool, and
+ *   ULYSSES_MASK_CAUSAL: s <= p and, when window > 0, s > p - window;
+ *   ULYSSES_MASK_NONE:   every such key (window must be 0).
+ * An entry of block_table outside [0, num_pages) holds no keys (a page given back behind a window);
+ * keys past max_pages * page_size do not exist. What lies in the pages behind kv_lens[i] is never
+ * used, NaN and infinities included; K and V of tokens below kv_lens[i] must be finite where V's
+ * weight is zero. Query head h attends with key/value head h / (H / H_kv).
+ * q: [T][H][d_h] bf16, rows q_stride elements apart (a multiple of 8, at least H * d_h);
+ * o: [T][H][d_h] bf16; lse: [H][T] fp32. A row with no permitted key gets o = 0 and lse = -inf.
+ * max_q: an upper bound of n_i where the caller knows one (1 when decoding), else 0: it chooses
+ * the kernels, and the results are right whatever it says. softmax_scale <= 0 selects
+ * 1 / sqrt(d_h). Row starts must ascend; ones outside [0, T] are clamped, lengths to [0, 2^30].
+ * Supported: d_h in {64, 128}, H % H_kv == 0, H / H_kv <= 128, T and max_pages * page_size up to
+ * 2^30; block-sparse masks are not.
+ * workspace: ulysses_paged_attn_workspace_size() bytes of the same H, H_kv, d_h and max_q, 256-byte
+ * aligned, contents need not be initialised; calls whose work overlaps on the GPU need their own.
+ * The size does not depend on lengths, T or B. Results are deterministic on one GPU model. */
+size_t ulysses_paged_attn_workspace_size(int H, int H_kv, int d_h, int max_q);
+int ulysses_paged_attn_fwd(const ulysses_kv_cache_t *cache, int B, int T, int H, int max_q, int mask_kind, int window,
+                           float softmax_scale, const void *q, int64_t q_stride, const int32_t *cu_q,
+                           const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride, int max_pages,
+                           void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Host helper: the block-sparse pattern "sliding window plus strided global key tiles".
  * Query tile qt gets key tiles max(0, qt - window_before) .. min(n - 1, qt + window_after)

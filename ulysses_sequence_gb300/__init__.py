@@ -36,11 +36,19 @@ class MaskStruct(ctypes.Structure):
                 ("nnz", ctypes.c_int)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    """ulysses_kv_cache_t; strides in elements."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("d_h", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 EXPORTS = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_kv_seq_to_head", "ulysses_kv_head_to_seq_sum",
            "ulysses_a2a_pack", "ulysses_a2a_unpack",
            "ulysses_qkv_proj", "ulysses_out_proj", "ulysses_usp_workspace_size", "ulysses_usp_attn_fwd",
            "ulysses_usp_attn_bwd", "ulysses_attn_fwd", "ulysses_attn_bwd_workspace_size",
            "ulysses_attn_bwd", "ulysses_attn_bwd_noalloc", "ulysses_bsmask_build_window_global",
+           "ulysses_page_plan", "ulysses_kv_append", "ulysses_paged_attn_workspace_size", "ulysses_paged_attn_fwd",
            "ulysses_get_device_status", "ulysses_selftest_timeout", "ulysses_status_string", "ulysses_shutdown")
 BWD_NOALLOC_SCRATCH_BYTES = 96 * 1024 * 1024  # ULYSSES_BWD_NOALLOC_SCRATCH_BYTES
 
@@ -78,13 +86,20 @@ def load() -> ctypes.CDLL:
                                              vp, vp]
     ip = ctypes.POINTER(ctypes.c_int32)
     lib.ulysses_bsmask_build_window_global.argtypes = [i, i, i, i, i, ip, ip, ip, ip, ctypes.POINTER(ctypes.c_int)]
+    i64, cp = ctypes.c_int64, ctypes.POINTER(KVCacheStruct)
+    lib.ulysses_page_plan.argtypes = [i, i, i, i, i64, i, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, vp]
+    lib.ulysses_kv_append.argtypes = [cp, i, vp, i64, vp, i64, vp, vp]
+    lib.ulysses_paged_attn_workspace_size.argtypes = [i, i, i, i]
+    lib.ulysses_paged_attn_workspace_size.restype = sz
+    lib.ulysses_paged_attn_fwd.argtypes = [cp, i, i, i, i, i, i, f, vp, i64, vp, vp, vp, i64, i, vp, vp, vp, sz, vp]
     lib.ulysses_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.ulysses_selftest_timeout.argtypes = [vp]
     lib.ulysses_status_string.argtypes = [i]
     lib.ulysses_shutdown.argtypes = []
     lib.ulysses_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
-        if name not in ("ulysses_attn_bwd_workspace_size", "ulysses_usp_workspace_size", "ulysses_status_string"):
+        if name not in ("ulysses_attn_bwd_workspace_size", "ulysses_usp_workspace_size",
+                        "ulysses_paged_attn_workspace_size", "ulysses_status_string"):
             getattr(lib, name).restype = i
     _lib = lib
     return lib
@@ -187,6 +202,32 @@ def ulysses_bsmask_build_window_global(L: int, tile: int, window_before: int, wi
                                                 ctypes.byref(nnz))
     check(rc, "ulysses_bsmask_build_window_global")
     return list(rp), list(kc)[:cap], list(cp), list(qr)[:cap]
+
+
+def ulysses_page_plan(B: int, T: int, page_size: int, max_pages: int, table_stride: int, num_pages: int,
+                      cached_lens: int, new_lens: int, free_pages: int, free_capacity: int, n_free: int,
+                      block_table: int, cu_q: int, kv_lens: int, slot_map: int, info: int, stream: int) -> int:
+    return load().ulysses_page_plan(B, T, page_size, max_pages, table_stride, num_pages, cached_lens, new_lens,
+                                    free_pages, free_capacity, n_free, block_table, cu_q, kv_lens, slot_map, info,
+                                    stream)
+
+
+def ulysses_kv_append(cache: Optional[KVCacheStruct], T: int, k: int, k_stride: int, v: int, v_stride: int,
+                      slot_map: int, stream: int) -> int:
+    return load().ulysses_kv_append(_mref(cache), T, k, k_stride, v, v_stride, slot_map, stream)
+
+
+def ulysses_paged_attn_workspace_size(H: int, H_kv: int, d_h: int, max_q: int) -> int:
+    return load().ulysses_paged_attn_workspace_size(H, H_kv, d_h, max_q)
+
+
+def ulysses_paged_attn_fwd(cache: Optional[KVCacheStruct], B: int, T: int, H: int, max_q: int, mask_kind: int,
+                           window: int, softmax_scale: float, q: int, q_stride: int, cu_q: int, kv_lens: int,
+                           block_table: int, table_stride: int, max_pages: int, o: int, lse: int, workspace: int,
+                           workspace_bytes: int, stream: int) -> int:
+    return load().ulysses_paged_attn_fwd(_mref(cache), B, T, H, max_q, mask_kind, window, softmax_scale, q, q_stride,
+                                         cu_q, kv_lens, block_table, table_stride, max_pages, o, lse, workspace,
+                                         workspace_bytes, stream)
 
 
 def ulysses_get_device_status(stream: int) -> Tuple[int, int]:
@@ -456,6 +497,174 @@ def attn_bwd(q, k, v, o, lse, do, P: int, mask: Mask, layout: int = LAYOUT_TOKEN
                            lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
                            ws.numel(), _stream(stream)), "attn_bwd")
     return dq, dk, dv
+
+
+# ----------------------------------------------------------------------------- paged cache
+
+class _on:
+    """The device and stream of one call: makes x's device current and, where the caller named a
+    stream, that stream too, so that what the call allocates belongs to it."""
+
+    def __init__(self, x, stream, where: str):
+        import torch
+        _require(x.is_cuda, where, "tensors must be on a CUDA device")
+        if stream is not None:
+            _require(stream.device == x.device, where, f"the stream is on {stream.device}, the tensors on {x.device}")
+        self.device = torch.cuda.device(x.device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self) -> int:
+        import torch
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return int(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _require(ok: bool, where: str, what: str) -> None:
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _i32_vector(x, n: int, name: str, like, where: str) -> None:
+    """x is a contiguous int32 vector of n entries on like's device."""
+    import torch
+    _require(x.dtype == torch.int32 and x.dim() == 1 and x.shape[0] == n and (n < 2 or x.stride(0) == 1), where,
+             f"{name} must be a contiguous int32 vector of {n} entries, got {x.dtype} {tuple(x.shape)}")
+    _require(x.device == like.device, where, f"{name} is on {x.device}, not on {like.device}")
+
+
+def _i32_table(x, B: int, like, where: str) -> int:
+    """Row stride of an int32 block table [B][max_pages] with contiguous rows on like's device."""
+    import torch
+    _require(x.dtype == torch.int32 and x.dim() == 2 and x.shape[0] == B
+             and (x.numel() == 0 or x.shape[1] == 1 or x.stride(1) == 1),
+             where, f"block_table must be int32 [{B}][max_pages] with contiguous rows, got {x.dtype} {tuple(x.shape)}")
+    _require(x.device == like.device, where, f"block_table is on {x.device}, not on {like.device}")
+    return x.stride(0) if B > 1 else x.shape[1]
+
+
+def _rows(x, T: int, heads: int, d: int, name: str, like, where: str) -> int:
+    """Row stride of bf16 token rows [T][heads][d] whose rows are contiguous, on like's device."""
+    import torch
+    _require(x.dtype == torch.bfloat16 and tuple(x.shape) == (T, heads, d)
+             and (x.numel() == 0 or (x.stride(2) == 1 and (heads == 1 or x.stride(1) == d))), where,
+             f"{name} must be bf16 [{T}][{heads}][{d}] with contiguous rows, got {x.dtype} {tuple(x.shape)}"
+             f" with strides {x.stride()}")
+    _require(x.device == like.device, where, f"{name} is on {x.device}, not on {like.device}")
+    return x.stride(0) if T > 1 else heads * d
+
+
+class PagedCache:
+    """A pool of key/value pages for the C ABI: k and v bf16 [num_pages][page_size][H_kv][d] with equal
+    strides and contiguous heads (any order of the first three dimensions in memory)."""
+
+    def __init__(self, k, v):
+        import torch
+        where = "PagedCache"
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(), where,
+                 "k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
+        _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.stride(3) == 1, where,
+                 "k and v must be bf16 with contiguous heads")
+        _require(k.is_cuda and k.device == v.device, where, "k and v must be on one CUDA device")
+        self.k, self.v = k, v
+        self.num_pages, self.page_size, self.H_kv, self.d = k.shape
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, k.stride(0), k.stride(1), k.stride(2))
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, H_kv: int, d: int, device="cuda") -> "PagedCache":
+        """A pool in the token layout, its contents undefined (unwritten entries are never used)."""
+        import torch
+        return PagedCache(*(torch.empty((num_pages, page_size, H_kv, d), dtype=torch.bfloat16, device=device)
+                            for _ in range(2)))
+
+
+def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size: int, num_pages: int, T: int, cu_q=None,
+              kv_lens=None, slot_map=None, info=None, stream=None):
+    """Block tables and slot maps of one step from request lengths, on the GPU (all int32): B requests hold
+    cached_lens[B] tokens and add new_lens[B]; new pages come from the end of free_pages[: n_free[0]] and
+    are written into block_table [B][max_pages] in place. Returns (cu_q [B+1], kv_lens [B], slot_map [T],
+    info [4] = rows planned, pages taken, pages missing, tokens dropped). The list is not changed:
+    ``n_free -= info[1:2]`` keeps the pages."""
+    import torch
+    where, B = "page_plan", block_table.shape[0]
+    table_stride = _i32_table(block_table, B, block_table, where)
+    for name, x, n in (("cached_lens", cached_lens, B), ("new_lens", new_lens, B), ("n_free", n_free, 1),
+                       ("free_pages", free_pages, free_pages.numel())):
+        _i32_vector(x, n, name, block_table, where)
+    with _on(block_table, stream, where) as st:
+        def out(x, n, name):
+            if x is None:
+                return torch.empty(n, dtype=torch.int32, device=block_table.device)
+            _i32_vector(x, n, name, block_table, where)
+            return x
+        cu_q, kv_lens = out(cu_q, B + 1, "cu_q"), out(kv_lens, B, "kv_lens")
+        slot_map, info = out(slot_map, T, "slot_map"), out(info, 4, "info")
+        check(ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
+                                new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                                block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
+                                info.data_ptr(), st), where)
+    return cu_q, kv_lens, slot_map, info
+
+
+def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
+    """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
+    fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
+    where, T = "kv_append", k.shape[0]
+    k_stride = _rows(k, T, cache.H_kv, cache.d, "k", cache.k, where)
+    v_stride = _rows(v, T, cache.H_kv, cache.d, "v", cache.k, where)
+    _i32_vector(slot_map, T, "slot_map", cache.k, where)
+    with _on(cache.k, stream, where) as st:
+        check(ulysses_kv_append(cache.struct, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
+                                st), where)
+
+
+def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
+    """Workspace of paged_attn_fwd for q [T][H][d]; its size depends on H, d and max_q alone, so one serves every
+    step of a program. Calls that may overlap on the GPU need one each."""
+    import torch
+    n = ulysses_paged_attn_workspace_size(q.shape[1], cache.H_kv, cache.d, max_q)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int = 0, mask: Optional[Mask] = None,
+                   window: int = 0, scale: float = 0.0, o=None, lse=None, workspace=None, stream=None):
+    """Attention of packed new tokens q bf16 [T][H][d] (request i owns rows cu_q[i] .. cu_q[i+1]) over the pages that
+    block_table [B][max_pages] names, kv_lens[B] keys each, the new tokens last. mask: Mask.causal() (the default)
+    by position, with an optional sliding window, or Mask.none(). max_q bounds the new tokens of a request where
+    known (1 when decoding; 0: unknown). Returns (o bf16 [T][H][d], lse fp32 [H][T]); rows behind the last
+    request are left as they were."""
+    import torch
+    where = "paged_attn_fwd"
+    _require(q.dim() == 3, where, f"q must be [T][H][d], got {tuple(q.shape)}")
+    T, H, d = q.shape
+    B = block_table.shape[0]
+    q_stride = _rows(q, T, H, cache.d, "q", cache.k, where)
+    table_stride = _i32_table(block_table, B, q, where)
+    _i32_vector(cu_q, B + 1, "cu_q", q, where)
+    _i32_vector(kv_lens, B, "kv_lens", q, where)
+    mask = Mask.causal() if mask is None else mask
+    with _on(q, stream, where) as st:
+        if o is None:
+            o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        _require(o.dtype == torch.bfloat16 and tuple(o.shape) == (T, H, d) and o.is_contiguous() and o.device == q.device,
+                 where, f"o must be contiguous bf16 {(T, H, d)} on {q.device}")
+        _require(lse.dtype == torch.float32 and tuple(lse.shape) == (H, T) and lse.is_contiguous()
+                 and lse.device == q.device, where, f"lse must be contiguous fp32 {(H, T)} on {q.device}")
+        ws = paged_attn_workspace(q, cache, max_q) if workspace is None else workspace
+        _require(ws.device == q.device and ws.is_contiguous(), where, f"workspace must be contiguous on {q.device}")
+        check(ulysses_paged_attn_fwd(cache.struct, B, T, H, max_q, mask.kind, window, scale, q.data_ptr(), q_stride,
+                                     cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), table_stride,
+                                     block_table.shape[1], o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), st), where)
+    return o, lse
 
 
 def shutdown() -> None:

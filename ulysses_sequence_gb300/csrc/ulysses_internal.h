@@ -111,6 +111,36 @@ int launch_usp_bwd(const ulysses_shape_t& s, int P_ring, const MaskArgs& m, floa
 int launch_proj_gemm(int M, int N, int K, const void* a, const void* b, int n_out, const int* col0, void* const* out,
                      const int* ld, cudaStream_t stream);
 
+// ---- serving from a paged key/value cache
+constexpr int kPlanMaxB = 8192;       // requests of one page plan (its prefix sums live in shared memory)
+constexpr int kPagedMaxLen = 1 << 30; // keys of a request, rows of a call: sums of two fit an int32
+constexpr int kPagedMaxGroup = 128;   // query heads per key/value head of the paged attention (one tile's rows)
+
+int launch_page_plan(int B, int T, int page_shift, int max_pages, int64_t table_stride, int num_pages,
+                     const int32_t* cached, const int32_t* fresh, const int32_t* free_pages, int free_capacity,
+                     const int32_t* n_free, int32_t* table, int32_t* cu_q, int32_t* kv_lens, int32_t* slots,
+                     int32_t* info, cudaStream_t stream);
+int launch_kv_append(const ulysses_kv_cache_t& c, int T, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int32_t* slots, cudaStream_t stream);
+
+// One paged attention call, validated.
+struct PagedAttnArgs {
+    ulysses_kv_cache_t cache;
+    int B, T, H, max_q, window;
+    bool causal;
+    float scale;
+    const void* q;
+    int64_t q_stride;
+    const int32_t *cu_q, *kv_lens, *table;
+    int64_t table_stride;
+    int max_pages;
+    void* o;
+    float* lse;
+    void* workspace;
+};
+size_t paged_attn_workspace_bytes(int H, int H_kv, int d_h, int max_q);
+int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
 inline int gcd_int(int a, int b) {
     while (b) { int t = a % b; a = b; b = t; }
     return a;
