@@ -501,63 +501,62 @@ def attn_bwd(q, k, v, o, lse, do, P: int, mask: Mask, layout: int = LAYOUT_TOKEN
 
 # ----------------------------------------------------------------------------- paged cache
 
-class _on:
-    """The device and stream of one call: makes x's device current and, where the caller named a
-    stream, that stream too, so that what the call allocates belongs to it."""
+# The paged calls are small enough for the host's work to show: their checks are plain conditions, and a
+# message is put together only when one fails.
 
-    def __init__(self, x, stream, where: str):
-        import torch
-        _require(x.is_cuda, where, "tensors must be on a CUDA device")
-        if stream is not None:
-            _require(stream.device == x.device, where, f"the stream is on {stream.device}, the tensors on {x.device}")
-        self.device = torch.cuda.device(x.device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self) -> int:
-        import torch
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return int(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
-
-
-def _require(ok: bool, where: str, what: str) -> None:
-    if not ok:
-        raise ValueError(f"{where}: {what}")
-
-
-def _i32_vector(x, n: int, name: str, like, where: str) -> None:
-    """x is a contiguous int32 vector of n entries on like's device."""
+def _call_stream(x, stream, where: str) -> int:
+    """The CUDA stream of one call on x's device, which must be the current one: the caller's, or the
+    current stream."""
     import torch
-    _require(x.dtype == torch.int32 and x.dim() == 1 and x.shape[0] == n and (n < 2 or x.stride(0) == 1), where,
-             f"{name} must be a contiguous int32 vector of {n} entries, got {x.dtype} {tuple(x.shape)}")
-    _require(x.device == like.device, where, f"{name} is on {x.device}, not on {like.device}")
+    if not x.is_cuda:
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device != x.device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {x.device}")
+    return stream.cuda_stream
 
 
-def _i32_table(x, B: int, like, where: str) -> int:
-    """Row stride of an int32 block table [B][max_pages] with contiguous rows on like's device."""
+def _new(shape, dtype, like, stream):
+    """An output allocated for the stream of the call, so that its memory is not reused before the call has run."""
     import torch
-    _require(x.dtype == torch.int32 and x.dim() == 2 and x.shape[0] == B
-             and (x.numel() == 0 or x.shape[1] == 1 or x.stride(1) == 1),
-             where, f"block_table must be int32 [{B}][max_pages] with contiguous rows, got {x.dtype} {tuple(x.shape)}")
-    _require(x.device == like.device, where, f"block_table is on {x.device}, not on {like.device}")
-    return x.stride(0) if B > 1 else x.shape[1]
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _rows(x, T: int, heads: int, d: int, name: str, like, where: str) -> int:
-    """Row stride of bf16 token rows [T][heads][d] whose rows are contiguous, on like's device."""
+def _check_tensor(x, shape, dtype, device, name: str, where: str) -> None:
+    """x is contiguous, of this shape and type, on this device."""
+    if x.shape == shape and x.dtype is dtype and x.device == device and x.is_contiguous():
+        return
+    raise ValueError(f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on {device}, got {x.dtype} "
+                     f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
+
+
+def _check_table(x, B: int, device, where: str) -> int:
+    """Row stride of an int32 block table [B][max_pages] with contiguous rows on this device."""
     import torch
-    _require(x.dtype == torch.bfloat16 and tuple(x.shape) == (T, heads, d)
-             and (x.numel() == 0 or (x.stride(2) == 1 and (heads == 1 or x.stride(1) == d))), where,
-             f"{name} must be bf16 [{T}][{heads}][{d}] with contiguous rows, got {x.dtype} {tuple(x.shape)}"
-             f" with strides {x.stride()}")
-    _require(x.device == like.device, where, f"{name} is on {x.device}, not on {like.device}")
-    return x.stride(0) if T > 1 else heads * d
+    if (x.dtype is torch.int32 and x.dim() == 2 and x.shape[0] == B and x.device == device
+            and (x.shape[1] < 2 or B == 0 or x.stride(1) == 1)):
+        return x.stride(0) if B > 1 else x.shape[1]
+    raise ValueError(f"{where}: block_table must be int32 [{B}][max_pages] with contiguous rows on {device}, got "
+                     f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+
+
+def _check_rows(x, T: int, heads: int, d: int, device, name: str, where: str) -> int:
+    """Row stride of bf16 token rows [T][heads][d] whose rows are contiguous, on this device."""
+    import torch
+    if x.shape == (T, heads, d) and x.dtype is torch.bfloat16 and x.device == device:
+        if T == 0:
+            return heads * d
+        row, head, one = x.stride()
+        if one == 1 and (heads == 1 or head == d):
+            return row if T > 1 else heads * d
+    raise ValueError(f"{where}: {name} must be bf16 [{T}][{heads}][{d}] with contiguous rows on {device}, got {x.dtype} "
+                     f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
 class PagedCache:
@@ -566,13 +565,13 @@ class PagedCache:
 
     def __init__(self, k, v):
         import torch
-        where = "PagedCache"
-        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(), where,
-                 "k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
-        _require(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.stride(3) == 1, where,
-                 "k and v must be bf16 with contiguous heads")
-        _require(k.is_cuda and k.device == v.device, where, "k and v must be on one CUDA device")
-        self.k, self.v = k, v
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("PagedCache: k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
+        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.stride(3) != 1:
+            raise ValueError("PagedCache: k and v must be bf16 with contiguous heads")
+        if not k.is_cuda or k.device != v.device:
+            raise ValueError("PagedCache: k and v must be on one CUDA device")
+        self.k, self.v, self.device = k, v, k.device
         self.num_pages, self.page_size, self.H_kv, self.d = k.shape
         self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, k.stride(0), k.stride(1), k.stride(2))
 
@@ -592,36 +591,38 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     info [4] = rows planned, pages taken, pages missing, tokens dropped). The list is not changed:
     ``n_free -= info[1:2]`` keeps the pages."""
     import torch
-    where, B = "page_plan", block_table.shape[0]
-    table_stride = _i32_table(block_table, B, block_table, where)
-    for name, x, n in (("cached_lens", cached_lens, B), ("new_lens", new_lens, B), ("n_free", n_free, 1),
-                       ("free_pages", free_pages, free_pages.numel())):
-        _i32_vector(x, n, name, block_table, where)
-    with _on(block_table, stream, where) as st:
-        def out(x, n, name):
-            if x is None:
-                return torch.empty(n, dtype=torch.int32, device=block_table.device)
-            _i32_vector(x, n, name, block_table, where)
-            return x
-        cu_q, kv_lens = out(cu_q, B + 1, "cu_q"), out(kv_lens, B, "kv_lens")
-        slot_map, info = out(slot_map, T, "slot_map"), out(info, 4, "info")
-        check(ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
-                                new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                                block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
-                                info.data_ptr(), st), where)
+    where, B, dev, i32 = "page_plan", block_table.shape[0], block_table.device, torch.int32
+    table_stride = _check_table(block_table, B, dev, where)
+    _check_tensor(cached_lens, (B,), i32, dev, "cached_lens", where)
+    _check_tensor(new_lens, (B,), i32, dev, "new_lens", where)
+    _check_tensor(n_free, (1,), i32, dev, "n_free", where)
+    _check_tensor(free_pages, (free_pages.numel(),), i32, dev, "free_pages", where)
+    st = _call_stream(block_table, stream, where)
+    outs = []
+    for name, x, n in (("cu_q", cu_q, B + 1), ("kv_lens", kv_lens, B), ("slot_map", slot_map, T), ("info", info, 4)):
+        if x is None:
+            x = _new((n,), i32, block_table, stream)
+        else:
+            _check_tensor(x, (n,), i32, dev, name, where)
+        outs.append(x)
+    cu_q, kv_lens, slot_map, info = outs
+    check(ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
+                            new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                            block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
+                            info.data_ptr(), st), where)
     return cu_q, kv_lens, slot_map, info
 
 
 def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
     """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
     fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
-    where, T = "kv_append", k.shape[0]
-    k_stride = _rows(k, T, cache.H_kv, cache.d, "k", cache.k, where)
-    v_stride = _rows(v, T, cache.H_kv, cache.d, "v", cache.k, where)
-    _i32_vector(slot_map, T, "slot_map", cache.k, where)
-    with _on(cache.k, stream, where) as st:
-        check(ulysses_kv_append(cache.struct, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
-                                st), where)
+    import torch
+    where, T, dev = "kv_append", k.shape[0], cache.device
+    k_stride = _check_rows(k, T, cache.H_kv, cache.d, dev, "k", where)
+    v_stride = _check_rows(v, T, cache.H_kv, cache.d, dev, "v", where)
+    _check_tensor(slot_map, (T,), torch.int32, dev, "slot_map", where)
+    check(ulysses_kv_append(cache.struct, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
+                            _call_stream(cache.k, stream, where)), where)
 
 
 def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
@@ -640,30 +641,33 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
     known (1 when decoding; 0: unknown). Returns (o bf16 [T][H][d], lse fp32 [H][T]); rows behind the last
     request are left as they were."""
     import torch
-    where = "paged_attn_fwd"
-    _require(q.dim() == 3, where, f"q must be [T][H][d], got {tuple(q.shape)}")
+    where, dev = "paged_attn_fwd", cache.device
+    if q.dim() != 3:
+        raise ValueError(f"{where}: q must be [T][H][d], got {tuple(q.shape)}")
     T, H, d = q.shape
     B = block_table.shape[0]
-    q_stride = _rows(q, T, H, cache.d, "q", cache.k, where)
-    table_stride = _i32_table(block_table, B, q, where)
-    _i32_vector(cu_q, B + 1, "cu_q", q, where)
-    _i32_vector(kv_lens, B, "kv_lens", q, where)
-    mask = Mask.causal() if mask is None else mask
-    with _on(q, stream, where) as st:
-        if o is None:
-            o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-        _require(o.dtype == torch.bfloat16 and tuple(o.shape) == (T, H, d) and o.is_contiguous() and o.device == q.device,
-                 where, f"o must be contiguous bf16 {(T, H, d)} on {q.device}")
-        _require(lse.dtype == torch.float32 and tuple(lse.shape) == (H, T) and lse.is_contiguous()
-                 and lse.device == q.device, where, f"lse must be contiguous fp32 {(H, T)} on {q.device}")
-        ws = paged_attn_workspace(q, cache, max_q) if workspace is None else workspace
-        _require(ws.device == q.device and ws.is_contiguous(), where, f"workspace must be contiguous on {q.device}")
-        check(ulysses_paged_attn_fwd(cache.struct, B, T, H, max_q, mask.kind, window, scale, q.data_ptr(), q_stride,
-                                     cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), table_stride,
-                                     block_table.shape[1], o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), st), where)
+    q_stride = _check_rows(q, T, H, cache.d, dev, "q", where)
+    table_stride = _check_table(block_table, B, dev, where)
+    _check_tensor(cu_q, (B + 1,), torch.int32, dev, "cu_q", where)
+    _check_tensor(kv_lens, (B,), torch.int32, dev, "kv_lens", where)
+    st = _call_stream(q, stream, where)
+    if o is None:
+        o = _new((T, H, d), torch.bfloat16, q, stream)
+    else:
+        _check_tensor(o, (T, H, d), torch.bfloat16, dev, "o", where)
+    if lse is None:
+        lse = _new((H, T), torch.float32, q, stream)
+    else:
+        _check_tensor(lse, (H, T), torch.float32, dev, "lse", where)
+    if workspace is None:
+        n = ulysses_paged_attn_workspace_size(H, cache.H_kv, d, max_q)
+        workspace = _new((max(n, 256),), torch.uint8, q, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous on {dev}")
+    check(ulysses_paged_attn_fwd(cache.struct, B, T, H, max_q, MASK_CAUSAL if mask is None else mask.kind, window, scale,
+                                 q.data_ptr(), q_stride, cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+                                 table_stride, block_table.shape[1], o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), st), where)
     return o, lse
 
 
