@@ -22,7 +22,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I" + os.path.join(ROOT, "include")] + ARCH
 SOURCES = ["api.cu", "relayout.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_noalloc.cu", "proj.cu", "usp.cu",
-           "paged_api.cu", "paged_plan.cu", "paged_attn.cu", "paged_decode.cu"]
+           "paged_api.cu", "paged_plan.cu", "paged_attn.cu", "paged_decode.cu",
+           "paged_chunk.cu"]
 
 
 def nvcc() -> str:

@@ -1,77 +1,32 @@
-// Attention of new tokens over a paged key/value cache, one warp per (row, query head): each lane
-// holds d / 32 elements of q and o, and the row's keys are visited one by one with a running
-// maximum and sum.
-#include <algorithm>
-
+// Dispatch of the paged attention: requests whose rows (new tokens x grouped query heads) fit one 16-row
+// fragment go to the decode kernel, the others to the chunk kernel. Which request is which is known on
+// the device only, so a call launches both, each passing over the other's requests, unless the
+// caller's bound on new tokens says that the decode kernel's are all (it then takes every request,
+// however long: the bound chooses, it does not decide what is computed) or the group is too wide for it.
 #include "paged_common.cuh"
 
 namespace ulysses {
 
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn_simple_kernel(const PagedParams p, const ulysses_kv_cache_t c) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.y, hk = h / p.G;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= p.T) return;
-    PagedSeq sq{};
-    int b = -1;
-    for (int i = 0; i < p.B && b < 0; ++i) {
-        sq = paged_seq(p, i);
-        if (row >= sq.start && row < sq.start + sq.n) b = i;
-    }
-    if (b < 0) return;
-    const int kv = sq.kv, pos = sq.base + (row - sq.start);
-    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(c.k), *vp = static_cast<const __nv_bfloat16*>(c.v);
-    int lo = 0, hi = kv;
-    if (p.causal) {
-        hi = min(kv, pos + 1);
-        if (p.window > 0) lo = max(0, pos - p.window + 1);
-    }
-    float q[E], o[E];
-    const __nv_bfloat16* qr = p.q + row * p.q_stride + h * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(qr[e]) * p.scale_log2;
-        o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int s = lo; s < hi; ++s) {
-        const int page = p.table[b * p.table_stride + (s >> p.page_shift)];
-        if (unsigned(page) >= unsigned(p.num_pages)) continue;
-        const int64_t off = page * c.page_stride + (s & ((1 << p.page_shift) - 1)) * c.token_stride +
-                            hk * c.head_stride + lane * E;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x += q[e] * __bfloat162float(kp[off + e]);
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-        const float mn = fmaxf(m, x);
-        const float a = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float w = mn == -INFINITY ? 0.f : exp2f(x - mn);
-        m = mn;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * __bfloat162float(vp[off + e]);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* orow = p.o + (int64_t(row) * p.H + h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) orow[e] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
+bool decode_fits(int G) { return G <= paged_decode_rows(); }
+bool decode_only(int G, int max_q) { return decode_fits(G) && max_q > 0 && int64_t(max_q) * G <= paged_decode_rows(); }
 
 }  // namespace
 
-// Requests whose rows (new tokens x grouped heads) fit the decode kernel's tile go there: all of them
-// when the caller's bound on new tokens says so, else those that do.
-static bool decode_only(int G, int max_q) {
-    return G <= paged_decode_rows() && max_q > 0 && int64_t(max_q) * G <= paged_decode_rows();
+bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks) {
+    cuuint64_t dims[5] = {64, cuuint64_t(c.page_size), cuuint64_t(c.H_kv), cuuint64_t(c.num_pages), cuuint64_t(c.d_h / 64)};
+    cuuint64_t strides[4] = {cuuint64_t(c.token_stride) * 2, cuuint64_t(c.head_stride) * 2, cuuint64_t(c.page_stride) * 2, 128};
+    cuuint32_t box[5] = {64, cuuint32_t(rows), 1, 1, cuuint32_t(chunks)};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr);
 }
 
-size_t paged_attn_workspace_bytes(int, int, int d_h, int) { return paged_decode_workspace_bytes(d_h); }
+size_t paged_attn_workspace_bytes(int H, int H_kv, int d_h, int max_q) {
+    const int G = H / H_kv;
+    return (decode_fits(G) ? paged_decode_workspace_bytes(d_h) : 0) +
+           (decode_only(G, max_q) ? 0 : paged_chunk_workspace_bytes(d_h));
+}
 
 int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     PagedParams p{};
@@ -87,22 +42,18 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.lse = a.lse;
     p.err = device_error_word();
     if (!p.err) return ULYSSES_ERR_CUDA;
-    if (a.H > 65535) return ULYSSES_ERR_UNSUPPORTED;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const bool only = decode_only(p.G, a.max_q);
-    if (p.G <= paged_decode_rows()) {
-        p.min_rows = 1;
+    p.min_rows = 1;
+    if (decode_fits(p.G)) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
-        const int rc = launch_paged_decode(a, p, a.workspace, stream);
+        const int rc = launch_paged_decode(a, p, ws, stream);
         if (rc != ULYSSES_OK || only) return rc;
         p.min_rows = paged_decode_rows() + 1;
-    } else {
-        p.min_rows = 1;
+        ws += paged_decode_workspace_bytes(a.cache.d_h);
     }
     p.max_rows = 0x7fffffff;
-    const dim3 grid((a.T + 3) / 4, a.H);
-    if (a.cache.d_h == 128) paged_attn_simple_kernel<128><<<grid, 128, 0, stream>>>(p, a.cache);
-    else paged_attn_simple_kernel<64><<<grid, 128, 0, stream>>>(p, a.cache);
-    return cudaGetLastError() == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
+    return launch_paged_chunk(a, p, ws, stream);
 }
 
 }  // namespace ulysses

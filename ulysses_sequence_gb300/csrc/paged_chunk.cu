@@ -1,0 +1,514 @@
+// Paged attention for chunks of new rows on the 5th-generation tensor cores (tcgen05, TMEM, TMA).
+//
+// A unit is up to 256 rows of one request with one key/value head: the rows of a token's grouped query
+// heads lie next to one another (row = token x G + head), so that every key/value tile brought into
+// shared memory serves all of them. Its two 128-row tiles share the key/value tiles, which halves their
+// traffic per product, and their softmax warpgroups alternate, so that the tensor core works on one
+// tile while the other's softmax runs. One CTA per SM walks its share of the batch's key tiles
+// (paged_common.cuh); the pipeline runs on across units: while a unit's rows are normalised and stored,
+// the next one's first scores are computed. Warp roles (320 threads):
+//   warp 0    producer: walks the share, looks up the pages (one lane per page copy) and keeps the Q, K
+//             and V copies going; publishes each piece (a unit's part in this CTA) and each tile's
+//             missing pages;
+//   warp 1    MMA issuer: S_t = Q_t K^T into TMEM columns [128 t, 128 t + 128) and O_t += P_t V into
+//             [256 + 128 t, ...), P_t read from the first 64 columns of S_t as packed bf16 pairs;
+//   warps 2-5 softmax of tile 0, warps 6-9 of tile 1: thread i owns row i (TMEM lane i). It takes the
+//             row maximum, writes the weights over the scores, rescales O_t when the maximum grew by
+//             more than 2^8, and stores the row at the end of the unit, or leaves it as a piece.
+// One thread issues PV_t of a key tile before S_t of the next, and its tcgen05 operations complete in
+// order: when S_t of a key tile is there, the previous PV_t is over, so O_t may be rescaled and S_t's
+// columns reused. A piece's first PV_t waits for that tile's weights, which its warps write only after
+// they have read the previous piece's O_t.
+// Values behind a request's last key may be anything: in the tile that holds the end, warps 2-5 clear
+// those rows of V in shared memory before the product reads them (0 x NaN is NaN).
+#include <algorithm>
+
+#include "paged_common.cuh"
+
+namespace ulysses {
+
+namespace {
+
+constexpr int kChunkThreads = 320;
+constexpr int kChunkRows = 2 * kTile;
+constexpr int kChunkMaxCtas = 160;   // one per SM: sizes the workspace
+constexpr int kChunkMinTiles = 4;    // key tiles below which another CTA costs more than it gives
+constexpr int kInfoRing = 8;         // tiles that the producer may describe ahead (it leads by at most 7)
+
+template <int D>
+struct ChunkCfg {
+    static constexpr int NSK = D == 64 ? 6 : 3;  // K and V pipeline stages
+    static constexpr int NSV = D == 64 ? 6 : 2;
+    static_assert(NSK + 1 < kInfoRing, "tile descriptions outlive their readers");
+    static constexpr uint32_t TILE_BYTES = kTile * D * 2;
+    static constexpr uint32_t CHUNK_BYTES = kTile * 128;  // 128 rows x 64 elements, swizzled
+    static constexpr uint32_t OFF_K = 2 * TILE_BYTES;
+    static constexpr uint32_t OFF_V = OFF_K + NSK * TILE_BYTES;
+    static constexpr uint32_t OFF_PIECE = OFF_V + NSV * TILE_BYTES;
+    static constexpr uint32_t OFF_INFO = OFF_PIECE + 128;
+    static constexpr uint32_t OFF_SH = OFF_INFO + kInfoRing * 4;
+    static constexpr uint32_t OFF_BAR = OFF_SH + 128;
+    static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
+    static constexpr uint32_t TMEM_COLS = 512;  // S0 | S1 | O0 | O1
+};
+
+// A unit's part in one CTA, as the producer describes it to the other warps.
+struct ChunkPiece {
+    int tiles, key0;        // key tiles, first key
+    int kv, pos;            // the request's keys, position of the unit's first token
+    int row0, tokens;       // first row of q, tokens of the unit
+    int head, slot;         // key/value head; slot of a piece or -1
+};
+static_assert(2 * sizeof(ChunkPiece) <= 128, "piece ring");
+
+constexpr uint32_t kInfoMasked = 0x100;  // some row does not see all of the tile; bits 0-7: pages of 16 keys that exist
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const PagedParams p, int log_rows /* of one page copy */) {
+    using C = ChunkCfg<D>;
+    constexpr int NSK = C::NSK, NSV = C::NSV;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
+    ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + C::OFF_PIECE);  // [2]
+    uint32_t* info = reinterpret_cast<uint32_t*>(smem + C::OFF_INFO);         // [kInfoRing]
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* k_full = q_empty + 1;         // [NSK]
+    uint64_t* k_empty = k_full + NSK;       // [NSK]
+    uint64_t* v_full = k_empty + NSK;       // [NSV]
+    uint64_t* v_empty = v_full + NSV;       // [NSV]
+    uint64_t* s_full = v_empty + NSV;       // [2]
+    uint64_t* p_full = s_full + 2;          // [2]
+    uint64_t* o_done = p_full + 2;          // [2]
+    uint64_t* piece_full = o_done + 2;      // [2]
+    uint64_t* piece_empty = piece_full + 2; // [2], MMA issuer and eight softmax warps
+    uint64_t* info_full = piece_empty + 2;  // [kInfoRing]
+    uint64_t* drain = info_full + kInfoRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+    const int warp = int(warp_id()), lane = int(lane_id());
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < NSK; ++i) {
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 1);
+        }
+        for (int i = 0; i < NSV; ++i) {
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + t, 1);
+            mbar_init(p_full + t, 4);
+            mbar_init(o_done + t, 1);
+            mbar_init(piece_full + t, 1);
+            mbar_init(piece_empty + t, 9);
+        }
+        for (int i = 0; i < kInfoRing; ++i) mbar_init(info_full + i, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    const int TOK = kTile / p.G, TQ = 2 * TOK;  // tokens of a tile, of a unit
+    PagedWalk<kTile> w;
+    const int n_ctas = paged_share<kTile, kChunkThreads>(p, TQ, kChunkMinTiles, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    const int cta = int(blockIdx.x);
+    __syncthreads();
+    if (cta >= n_ctas) {
+        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0, 0, 0};
+        return;
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Abort ab{abort_flag, p.err, KID_PAGED};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
+        // a copy is one page (or 128 keys of a longer one) by 64 elements, or by the whole head where one
+        // copy fills the tile; lane l copies page l / per, 64-element chunk l % per
+        const int per = log_rows == 7 ? 1 : D / 64;
+        const int copies = (kTile >> log_rows) * per;  // of one tile, at most 16
+        const int my_row = (lane / per) << log_rows;
+        const int my_chunk = lane % per;
+        auto lookup = [&](int key0) {
+            const int key = key0 + my_row;
+            return lane < copies && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
+        };
+        PagedMeta meta{0, 0, 0, 0, 0, 0};
+        int nk = 0, nv = 0, nq = 0, piece = 0;  // copies and pieces so far
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_LOAD, site));
+        };
+        while (ok && w.left > 0) {
+            // the next piece: what this CTA does of the walk's unit
+            const int tiles = int(min(int64_t(w.count - w.off), w.left));
+            const bool whole = w.off == 0, ends = w.off + tiles == w.count;
+            const int tokens = w.t1 - w.t0, row0 = w.s.start + w.t0, pos = w.s.base + w.t0;
+            const int key_first = (w.first + w.off) * kTile;
+            int slot = -1;
+            if (piece == 0 && !whole) {
+                slot = 2 * cta;
+                meta.cont = 1;
+                meta.ends = ends;
+            } else if (!ends) {
+                slot = 2 * cta + 1;
+                meta.opens = 1;
+                meta.head = w.head;
+                meta.row0 = row0;
+                meta.rows = tokens * p.G;
+            }
+            if (piece >= 2 && !(ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 1))) break;
+            if (lane == 0) {
+                pieces[piece & 1] = ChunkPiece{tiles, key_first, w.s.kv, pos, row0, tokens, w.head, slot};
+                mbar_arrive(piece_full + (piece & 1));
+            }
+            int id = lookup(key_first);
+            for (int i = 0; i < tiles; ++i) {
+                const int key0 = key_first + i * kTile;
+                const int id_next = i + 1 < tiles ? lookup(key0 + kTile) : -1;
+                const int sk = nk % NSK, sv = nv % NSV;
+                if (nk >= NSK && !(ok = wait(k_empty + sk, ((nk / NSK) - 1) & 1, 2))) break;
+                const bool good = unsigned(id) < unsigned(p.num_pages);
+                // a page that does not exist is copied from behind the pool: zeros
+                const int page = good ? id : p.num_pages, row = (key0 + my_row) & ((1 << p.page_shift) - 1);
+                const unsigned have = __ballot_sync(0xffffffffu, good && my_chunk == 0);
+                const int of = (min(lane, 7) * 16) >> log_rows;  // the copy of keys [16 lane, 16 lane + 16)
+                const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && ((have >> (of * per)) & 1u));
+                const uint32_t off = my_chunk * C::CHUNK_BYTES + my_row * 128;
+                if (lane == 0) {
+                    // clear: every row of the unit sees every key of the tile
+                    const bool clear = valid == 0xff && key0 + kTile <= w.s.kv &&
+                                       (!p.causal || (key0 + kTile <= pos + 1 && (p.window == 0 || key0 > pos + tokens - 1 - p.window)));
+                    info[nk % kInfoRing] = valid | (clear ? 0u : kInfoMasked);
+                    mbar_arrive(info_full + nk % kInfoRing);
+                    mbar_arrive_expect_tx(k_full + sk, C::TILE_BYTES);
+                }
+                __syncwarp();
+                if (lane < copies) tma_load_5d(sK + sk * C::TILE_BYTES + off, &tm_k, k_full + sk, 0, row, w.head, page, my_chunk);
+                ++nk;
+                if (i == 0) {
+                    // the unit's queries, once the previous piece's last scores are computed
+                    if (piece >= 1 && !(ok = wait(q_empty, (piece - 1) & 1, 3))) break;
+                    const int n_t = tokens > TOK ? 2 : 1;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, uint32_t(n_t * (D / 64)) * uint32_t(TOK * p.G) * 128u);
+                        for (int t = 0; t < n_t; ++t)
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_5d(sQ + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_q, q_full, 0, w.head * p.G,
+                                            row0 + t * TOK, c, 0);
+                    }
+                    __syncwarp();
+                    ++nq;
+                }
+                if (nv >= NSV && !(ok = wait(v_empty + sv, ((nv / NSV) - 1) & 1, 4))) break;
+                if (lane == 0) mbar_arrive_expect_tx(v_full + sv, C::TILE_BYTES);
+                __syncwarp();
+                if (lane < copies) tma_load_5d(sV + sv * C::TILE_BYTES + off, &tm_v, v_full + sv, 0, row, w.head, page, my_chunk);
+                ++nv;
+                id = id_next;
+            }
+            if (!ok) break;
+            ++piece;
+            w.left -= tiles;
+            if (w.left > 0) w.next_unit(p, TQ);
+        }
+        if (lane == 0) {
+            p.meta[cta] = meta;
+            if (!ok) {
+                // copies already in flight land before the CTA can exit
+                if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
+                for (int st = 0; st < NSK; ++st) {
+                    const int n = nk > st ? (nk - 1 - st) / NSK + 1 : 0;
+                    if (n > 0) mbar_drain(k_full + st, (n - 1) & 1);
+                }
+                for (int st = 0; st < NSV; ++st) {
+                    const int n = nv > st ? (nv - 1 - st) / NSV + 1 : 0;
+                    if (n > 0) mbar_drain(v_full + st, (n - 1) & 1);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+            const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+            auto issue_s = [&](int t, int sk) {  // S_t = Q_t K^T
+                const uint64_t dq = sdesc_sw128(aQ + t * C::TILE_BYTES, 16, 1024);
+                const uint64_t dk = sdesc_sw128(aK + sk * C::TILE_BYTES, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = (k >> 2) * C::CHUNK_BYTES + (k & 3) * 32;
+                    umma_ss(tmem + 128 * t, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
+                }
+                umma_commit(s_full + t);
+            };
+            auto issue_pv = [&](int t, int sv, bool first) {  // O_t (+)= P_t V
+                const uint64_t dv = sdesc_sw128(aV + sv * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)  // 16 keys = 8 TMEM columns of P per step
+                    umma_ts(tmem + 256 + 128 * t, tmem + 128 * t + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
+            };
+            bool ok = true;
+            int j = 0, c0 = 0, c1 = 0;  // key tiles so far, PV_t so far
+            int64_t left = w.left;
+            for (int piece = 0; ok && left > 0; ++piece) {
+                if (!(ok = mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_MMA, 1))) break;
+                const int n = pieces[piece & 1].tiles;
+                const bool two = pieces[piece & 1].tokens > TOK;
+                mbar_arrive(piece_empty + (piece & 1));
+                left -= n;
+                if (!(ok = mbar_wait(q_full, piece & 1, ab, ROLE_MMA, 2))) break;
+                if (!(ok = mbar_wait(k_full + j % NSK, (j / NSK) & 1, ab, ROLE_MMA, 3))) break;
+                tc_fence_after();
+                issue_s(0, j % NSK);
+                if (two) issue_s(1, j % NSK);
+                umma_commit(k_empty + j % NSK);
+                if (n == 1) umma_commit(q_empty);
+                for (int i = 0; i < n; ++i, ++j) {
+                    const bool next = i + 1 < n;
+                    const int sv = j % NSV, sk = (j + 1) % NSK;
+                    if (!(ok = mbar_wait(v_full + sv, (j / NSV) & 1, ab, ROLE_MMA, 4))) break;
+                    if (!(ok = mbar_wait(p_full, c0++ & 1, ab, ROLE_MMA, 5))) break;
+                    tc_fence_after();
+                    issue_pv(0, sv, i == 0);
+                    if (next) {
+                        if (!(ok = mbar_wait(k_full + sk, ((j + 1) / NSK) & 1, ab, ROLE_MMA, 6))) break;
+                        tc_fence_after();
+                        issue_s(0, sk);
+                    } else {
+                        umma_commit(o_done);
+                    }
+                    if (two) {
+                        if (!(ok = mbar_wait(p_full + 1, c1++ & 1, ab, ROLE_MMA, 7))) break;
+                        tc_fence_after();
+                        issue_pv(1, sv, i == 0);
+                        if (next) issue_s(1, sk);
+                        else umma_commit(o_done + 1);
+                    }
+                    if (next) umma_commit(k_empty + sk);
+                    if (i + 2 == n) umma_commit(q_empty);  // the piece's last scores are under way
+                    umma_commit(v_empty + sv);
+                }
+            }
+            if (!ok) {
+                umma_commit(drain);
+                mbar_drain(drain, 0);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------ softmax (tile t)
+        const int t = warp < 6 ? 0 : 1;
+        const int wq = warp & 3;                  // TMEM lane quadrant of this warp
+        const int row = wq * 32 + lane;           // row within the tile (TMEM lane)
+        const uint32_t lane_off = uint32_t(wq * 32) << 16;
+        const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + 256 + 128 * t + lane_off;
+        const int tok = row / p.G;                // the row's token within the tile
+        bool ok = true;
+        int j = 0, cs = 0, units = 0;             // key tiles so far; this tile's S and O so far
+        int64_t left = w.left;
+        for (int piece = 0; ok && left > 0; ++piece) {
+            ok = __all_sync(0xffffffffu, mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
+            if (!ok) break;
+            const ChunkPiece u = pieces[piece & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(piece_empty + (piece & 1));
+            left -= u.tiles;
+            const int my_tokens = min(TOK, u.tokens - t * TOK);
+            if (my_tokens <= 0) {  // the unit has one tile
+                j += u.tiles;
+                continue;
+            }
+            const bool valid = tok < my_tokens;
+            const int pos = u.pos + t * TOK + tok;
+            const int hi = p.causal ? max(0, min(u.kv, pos + 1)) : u.kv;     // the row sees keys [lo, hi)
+            const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            float m_used = -INFINITY, l_sum = 0.f;  // running maximum (log2 domain) and sum
+            for (int i = 0; i < u.tiles; ++i, ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, cs++ & 1, ab, ROLE_SOFTMAX, 2) &&
+                                                 mbar_wait(info_full + j % kInfoRing, (j / kInfoRing) & 1, ab, ROLE_SOFTMAX, 3));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t what = info[j % kInfoRing];
+                const bool masked = what & kInfoMasked;
+                const int key0 = u.key0 + i * kTile;
+                auto mask_half = [&](float* v, int c0) {
+                    if (masked) {
+                        const int h = hi - key0 - c0, b = lo - key0 - c0;
+                        const uint32_t pages = what >> (c0 / 16);
+#pragma unroll
+                        for (int x = 0; x < 64; ++x)
+                            if (x >= h || x < b || !((pages >> (x / 16)) & 1u)) v[x] = -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    float v[64];
+                    tmem_ld32(tS + hh * 64, v);
+                    tmem_ld32(tS + hh * 64 + 32, v + 32);
+                    tmem_wait_ld();
+                    mask_half(v, hh * 64);
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) mx = fmaxf(mx, v[x]);
+                }
+                const float m_new = fmaxf(m_used, mx * p.scale_log2);
+                const bool need = valid && m_new > m_used + 8.0f;
+                const float alpha = need ? ex2(m_used - m_new) : 1.0f;  // ex2(-inf) = 0 for a first maximum
+                if (need) m_used = m_new;
+                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                // the weights, rounded to bf16 for the matrix product (their sum is not), over the scores:
+                // half hh lands in columns [32 hh, 32 hh + 32), already read
+                float rs = 0.f;
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    float v[64];
+                    tmem_ld32(tS + hh * 64, v);
+                    tmem_ld32(tS + hh * 64 + 32, v + 32);
+                    tmem_wait_ld();
+                    mask_half(v, hh * 64);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float e0 = ex2(fmaf(v[2 * x], p.scale_log2, neg_m));
+                        const float e1 = ex2(fmaf(v[2 * x + 1], p.scale_log2, neg_m));
+                        rs += e0 + e1;
+                        pk[x] = pack_bf16(e0, e1);
+                    }
+                    tmem_st32_u(tS + hh * 32, pk);
+                }
+                l_sum = l_sum * alpha + rs;
+                if (i > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        float o[32];
+                        tmem_ld32(tO + x * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] *= alpha;
+                        tmem_st32(tO + x * 32, o);
+                    }
+                }
+                if (t == 0 && key0 + kTile > u.kv) {
+                    // clear the values behind the last key; tile 1's product follows tile 0's
+                    const int sv = j % NSV;
+                    ok = __all_sync(0xffffffffu, mbar_wait(v_full + sv, (j / NSV) & 1, ab, ROLE_SOFTMAX, 4));
+                    if (!ok) break;
+                    if (key0 + row >= u.kv) {
+                        const uint32_t a = smem_u32(sV + sv * C::TILE_BYTES) + row * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) st_shared_v4(a + c * C::CHUNK_BYTES + x * 16, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + t);
+            }
+            if (!ok) break;
+            // -------------------------------------------------------------- the piece's rows
+            ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, units++ & 1, ab, ROLE_EPI, 1));
+            if (!ok) break;
+            tc_fence_after();
+            const bool any_key = l_sum > 0.f;
+            const float inv = u.slot >= 0 ? 1.0f : (any_key ? 1.0f / l_sum : 0.f);
+            const int unit_row = t * TOK * p.G + row;
+            const int q_row = u.row0 + t * TOK + tok, h = u.head * p.G + row % p.G;
+            __nv_bfloat16* dst = p.o + (int64_t(q_row) * p.H + h) * D;
+            float* part = p.part_o + (int64_t(max(u.slot, 0)) * kChunkRows + unit_row) * D;
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+                float o[32];
+                tmem_ld32(tO + x * 32, o);
+                tmem_wait_ld();
+                if (!valid) continue;
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] *= inv;
+                if (u.slot >= 0) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        reinterpret_cast<float4*>(part + x * 32)[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        reinterpret_cast<uint4*>(dst + x * 32)[y] =
+                            make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
+                                       pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7]));
+                }
+            }
+            if (valid) {
+                if (u.slot >= 0) p.part_ml[int64_t(u.slot) * kChunkRows + unit_row] = make_float2(m_used, l_sum);
+                else p.lse[int64_t(h) * p.T + q_row] = any_key ? (m_used + log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int D>
+int launch_chunk_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaStream_t stream) {
+    using C = ChunkCfg<D>;
+    const int rows = std::min(a.cache.page_size, kTile);
+    const int chunks = rows == kTile ? D / 64 : 1;
+    CUtensorMap mq, mk, mv;
+    {
+        const int tok = kTile / p.G;
+        cuuint64_t dims[5] = {64, cuuint64_t(p.H), cuuint64_t(p.T), D / 64, 1};
+        cuuint64_t strides[4] = {D * 2, cuuint64_t(p.q_stride) * 2, 128, 128};
+        cuuint32_t box[5] = {64, cuuint32_t(p.G), cuuint32_t(tok), 1, 1};
+        cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+        if (!encode_tensor_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.q, dims, strides, box, estr)) return ULYSSES_ERR_CUDA;
+    }
+    if (!encode_pages(&mk, a.cache, a.cache.k, rows, chunks) || !encode_pages(&mv, a.cache, a.cache.v, rows, chunks))
+        return ULYSSES_ERR_CUDA;
+    auto kern = paged_chunk_kernel<D>;
+    if (!set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ULYSSES_ERR_CUDA;
+    const int ctas = std::min(device_sm_count(), kChunkMaxCtas);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    ws += size_t(2) * kChunkMaxCtas * kChunkRows * D * 4;
+    p.part_ml = reinterpret_cast<float2*>(ws);
+    ws += size_t(2) * kChunkMaxCtas * kChunkRows * 8;
+    p.meta = reinterpret_cast<PagedMeta*>(ws);
+    kern<<<ctas, kChunkThreads, C::SMEM_BYTES, stream>>>(mq, mk, mv, p, __builtin_ctz(unsigned(rows)));
+    if (cudaGetLastError() != cudaSuccess) return ULYSSES_ERR_CUDA;
+    return launch_paged_join<D, kChunkRows, 8>(p, ctas, stream);
+}
+
+}  // namespace
+
+size_t paged_chunk_workspace_bytes(int d_h) {
+    const size_t n = size_t(2) * kChunkMaxCtas * kChunkRows * (size_t(d_h) * 4 + 8) + kChunkMaxCtas * sizeof(PagedMeta);
+    return (n + 255) / 256 * 256;
+}
+
+int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream) {
+    return a.cache.d_h == 128 ? launch_chunk_d<128>(a, p, workspace, stream) : launch_chunk_d<64>(a, p, workspace, stream);
+}
+
+}  // namespace ulysses

@@ -293,9 +293,15 @@ inline int launch_paged_join(const PagedParams& p, int ctas, cudaStream_t stream
     return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS, NY>, p, ctas) == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 
-// Requests of few rows (paged_decode.cu).
+// Tensor map of a pool's keys or values, (64 elements, token, head, page, 64-element chunk), for copies
+// of `rows` tokens of one page and head by `chunks` chunks (chunk after chunk), 128-byte swizzle.
+bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks);
+
+// Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu).
 int paged_decode_rows();
 size_t paged_decode_workspace_bytes(int d_h);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream);
+size_t paged_chunk_workspace_bytes(int d_h);
+int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream);
 
 }  // namespace ulysses

@@ -391,14 +391,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     __syncthreads();
 }
 
-bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks) {
-    cuuint64_t dims[5] = {64, cuuint64_t(c.page_size), cuuint64_t(c.H_kv), cuuint64_t(c.num_pages), cuuint64_t(c.d_h / 64)};
-    cuuint64_t strides[4] = {cuuint64_t(c.token_stride) * 2, cuuint64_t(c.head_stride) * 2, cuuint64_t(c.page_stride) * 2, 128};
-    cuuint32_t box[5] = {64, cuuint32_t(rows), 1, 1, cuuint32_t(chunks)};
-    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr);
-}
-
 template <int D>
 int launch_decode_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaStream_t stream) {
     using C = DecodeCfg<D>;
