@@ -32,7 +32,8 @@ namespace {
 constexpr int kChunkThreads = 320;
 constexpr int kChunkRows = 2 * kTile;
 constexpr int kChunkMaxCtas = 160;   // one per SM: sizes the workspace
-constexpr int kChunkMinTiles = 4;    // key tiles below which another CTA costs more than it gives
+constexpr int kChunkMinCost = 4;     // share below which another CTA costs more than it gives
+constexpr int kChunkUnitCost = 2;    // fixed cost of a unit, in key tiles
 constexpr int kInfoRing = 8;         // tiles that the producer may describe ahead (it leads by at most 7)
 
 template <int D>
@@ -55,7 +56,7 @@ struct ChunkCfg {
 
 // A unit's part in one CTA, as the producer describes it to the other warps.
 struct ChunkPiece {
-    int tiles, key0;        // key tiles, first key
+    int tiles, key0;        // key tiles (0: the share is done), first key
     int kv, pos;            // the request's keys, position of the unit's first token
     int row0, tokens;       // first row of q, tokens of the unit
     int head, slot;         // key/value head; slot of a piece or -1
@@ -91,6 +92,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
+    grid_release();
     const int warp = int(warp_id()), lane = int(lane_id());
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -116,12 +118,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fence_mbar_init();
     }
     const int TOK = kTile / p.G, TQ = 2 * TOK;  // tokens of a tile, of a unit
-    PagedWalk<kTile> w;
-    const int n_ctas = paged_share<kTile, kChunkThreads>(p, TQ, kChunkMinTiles, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    PagedWalk<kTile, kChunkUnitCost> w;
     const int cta = int(blockIdx.x);
+    const bool work = paged_share<kTile, kChunkUnitCost, kChunkThreads>(p, TQ, kChunkMinCost,
+                                                                        reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     __syncthreads();
-    if (cta >= n_ctas) {
-        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0, 0, 0};
+    if (!work) {
+        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0};
         return;
     }
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -148,7 +151,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int key = key0 + my_row;
             return lane < copies && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
         };
-        PagedMeta meta{0, 0, 0, 0, 0, 0};
+        PagedMeta meta{0, 0, 0, 0};
         int nk = 0, nv = 0, nq = 0, piece = 0;  // copies and pieces so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
@@ -156,21 +159,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         while (ok && w.left > 0) {
             // the next piece: what this CTA does of the walk's unit
-            const int tiles = int(min(int64_t(w.count - w.off), w.left));
-            const bool whole = w.off == 0, ends = w.off + tiles == w.count;
+            int off, tiles;
+            w.take(off, tiles);
+            if (tiles == 0) {
+                if (w.left > 0) w.next_unit(p, TQ);
+                continue;
+            }
             const int tokens = w.t1 - w.t0, row0 = w.s.start + w.t0, pos = w.s.base + w.t0;
-            const int key_first = (w.first + w.off) * kTile;
+            const int key_first = (w.first + off) * kTile;
             int slot = -1;
-            if (piece == 0 && !whole) {
+            if (piece == 0 && off > 0) {
                 slot = 2 * cta;
-                meta.cont = 1;
-                meta.ends = ends;
-            } else if (!ends) {
+            } else if (off + tiles < w.count) {
                 slot = 2 * cta + 1;
-                meta.opens = 1;
-                meta.head = w.head;
-                meta.row0 = row0;
-                meta.rows = tokens * p.G;
+                meta = PagedMeta{w.pieces(cta), w.head, row0, tokens * p.G};
             }
             if (piece >= 2 && !(ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 1))) break;
             if (lane == 0) {
@@ -224,8 +226,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (!ok) break;
             ++piece;
-            w.left -= tiles;
             if (w.left > 0) w.next_unit(p, TQ);
+        }
+        if (ok && (piece < 2 || (ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 5))) && lane == 0) {
+            pieces[piece & 1].tiles = 0;
+            mbar_arrive(piece_full + (piece & 1));
         }
         if (lane == 0) {
             p.meta[cta] = meta;
@@ -266,13 +271,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             bool ok = true;
             int j = 0, c0 = 0, c1 = 0;  // key tiles so far, PV_t so far
-            int64_t left = w.left;
-            for (int piece = 0; ok && left > 0; ++piece) {
+            for (int piece = 0; ok; ++piece) {
                 if (!(ok = mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_MMA, 1))) break;
                 const int n = pieces[piece & 1].tiles;
                 const bool two = pieces[piece & 1].tokens > TOK;
+                if (n == 0) break;
                 mbar_arrive(piece_empty + (piece & 1));
-                left -= n;
                 if (!(ok = mbar_wait(q_full, piece & 1, ab, ROLE_MMA, 2))) break;
                 if (!(ok = mbar_wait(k_full + j % NSK, (j / NSK) & 1, ab, ROLE_MMA, 3))) break;
                 tc_fence_after();
@@ -321,14 +325,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int tok = row / p.G;                // the row's token within the tile
         bool ok = true;
         int j = 0, cs = 0, units = 0;             // key tiles so far; this tile's S and O so far
-        int64_t left = w.left;
-        for (int piece = 0; ok && left > 0; ++piece) {
+        for (int piece = 0; ok; ++piece) {
             ok = __all_sync(0xffffffffu, mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
             if (!ok) break;
             const ChunkPiece u = pieces[piece & 1];
+            if (u.tiles == 0) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(piece_empty + (piece & 1));
-            left -= u.tiles;
             const int my_tokens = min(TOK, u.tokens - t * TOK);
             if (my_tokens <= 0) {  // the unit has one tile
                 j += u.tiles;
@@ -497,7 +500,7 @@ int launch_chunk_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaS
     p.meta = reinterpret_cast<PagedMeta*>(ws);
     kern<<<ctas, kChunkThreads, C::SMEM_BYTES, stream>>>(mq, mk, mv, p, __builtin_ctz(unsigned(rows)));
     if (cudaGetLastError() != cudaSuccess) return ULYSSES_ERR_CUDA;
-    return launch_paged_join<D, kChunkRows, 8>(p, ctas, stream);
+    return launch_paged_join<D, kChunkRows>(p, ctas, stream);
 }
 
 }  // namespace

@@ -3,12 +3,12 @@
 //
 // A unit is one tile of a request's new rows with one key/value head; its rows are the unit's
 // tokens times the G query heads of that key/value head, so grouped heads read each key once. A
-// unit's work is its number of key tiles (at least one). All units, in the order request, head,
-// row tile, form one line of W key tiles, and CTA c of n takes [c W / n, (c + 1) W / n) of it:
-// every CTA gets the same number of key tiles whatever the lengths. A unit that a CTA boundary
-// cuts is finished by a second kernel, which joins its pieces by the online-softmax rule
-// (m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i, in fp32 and in the pieces' order). A
-// CTA leaves at most two pieces, so the workspace depends on the grid alone.
+// unit costs its number of key tiles (at least one) plus a fixed part for its queries and its rows'
+// way out, counted in key tiles. All units, in the order request, head, row tile, form one line of cost
+// W, and CTA c of n takes [c W / n, (c + 1) W / n) of it: every CTA gets the same cost whatever the
+// lengths. A unit that a CTA boundary cuts is finished by a second kernel, which joins its pieces by the
+// online-softmax rule (m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i, in fp32 and in the
+// pieces' order). A CTA leaves at most two pieces, so the workspace depends on the grid alone.
 #pragma once
 
 #include "common.cuh"
@@ -34,15 +34,11 @@ struct PagedParams {
     uint32_t* err;
 };
 
-// What the joining kernel knows of CTA c: a first piece that continues a unit is in slot 2 c, a last
-// piece that opens one in slot 2 c + 1.
+// What the joining kernel knows of CTA c: the unit that its last piece opens and later CTAs go on with. The
+// opening piece is in slot 2 c + 1, those of CTAs c + 1, ... in slots 2 (c + 1), ...
 struct PagedMeta {
-    int cont;    // the first piece continues a unit begun by an earlier CTA
-    int ends;    // ... and finishes it
-    int opens;   // the last piece begins a unit that a later CTA continues
-    int head;    // of the unit opened
-    int row0;    // its first row of q
-    int rows;    // its rows (tokens x G)
+    int pieces;  // of the unit, 0 where there is none
+    int head, row0, rows;
 };
 
 // The new rows [start, start + n) of request i, its keys [0, kv), and the position of row 0.
@@ -81,29 +77,45 @@ __device__ __forceinline__ void paged_tiles(const PagedParams& p, const PagedSeq
     count = max(1, (hi + KT - 1) / KT - first);
 }
 
-// Key tiles of one head of a request, over its row tiles of TQ tokens.
-template <int KT>
+// Cost of one head of a request, over its row tiles of TQ tokens; OVH is a unit's fixed part.
+template <int KT, int OVH>
 __device__ __forceinline__ int64_t paged_head_cost(const PagedParams& p, const PagedSeq& s, int TQ) {
     int64_t sum = 0;
     for (int t0 = 0; t0 < s.n; t0 += TQ) {
         int first, count;
         paged_tiles<KT>(p, s, t0, min(s.n, t0 + TQ), first, count);
-        sum += count;
+        sum += count + OVH;
     }
     return sum;
 }
 
-// One CTA's walk along the line of key tiles; the whole warp holds the same state.
-template <int KT>
+// One CTA's walk along the line; the whole warp holds the same state.
+template <int KT, int OVH>
 struct PagedWalk {
     int i, head, t0, t1;     // unit: request, key/value head, tokens [t0, t1)
     PagedSeq s;
-    int first, count, off;   // its key tiles, and the next one's offset among them
-    int64_t left;            // key tiles that this CTA still has to do
+    int first, count;        // its key tiles
+    int pos;                 // cost of it that lies behind
+    int64_t left;            // cost that this CTA still has to do
+    int64_t W;               // the line's cost
+    int n;                   // CTAs with work (the first ones)
 
     __device__ __forceinline__ void unit(const PagedParams& p, int TQ) {
         t1 = min(s.n, t0 + TQ);
         paged_tiles<KT>(p, s, t0, t1, first, count);
+    }
+    // This CTA's part of the unit, key tiles [off, off + tiles), possibly none.
+    __device__ __forceinline__ void take(int& off, int& tiles) {
+        const int end = int(min(int64_t(pos) + left, int64_t(OVH) + count));
+        off = max(0, pos - OVH);
+        tiles = max(0, end - OVH) - off;
+        left -= end - pos;
+        pos = end;
+    }
+    // Pieces of the unit from CTA c, which has just taken its end of the line and left some of the unit.
+    __device__ __forceinline__ int pieces(int c) const {
+        const int64_t unit_end = W * (c + 1) / n + (OVH + count - pos);
+        return int((unit_end * n + W - 1) / W) - c;  // the CTA whose end reaches the unit's, as an index past c
     }
     // The next request that has rows, 32 looked at at a time; only called while there is one.
     __device__ __forceinline__ void next_request(const PagedParams& p) {
@@ -125,7 +137,7 @@ struct PagedWalk {
         s.n = 0;
     }
     __device__ __forceinline__ void next_unit(const PagedParams& p, int TQ) {
-        off = 0;
+        pos = 0;
         t0 += TQ;
         if (t0 >= s.n) {
             t0 = 0;
@@ -138,61 +150,81 @@ struct PagedWalk {
     }
 };
 
-// Where this CTA's share of the line begins. All threads of the block call it (NT threads, a whole
-// number of warps); every warp leaves with the same walk. Returns the number of CTAs that have work
-// (the first ones); a CTA at or past it has none.
-template <int KT, int NT>
-__device__ __forceinline__ int paged_share(const PagedParams& p, int TQ, int min_tiles, int64_t* sh /* [NT / 32 + 4] */,
-                                           PagedWalk<KT>& w) {
+// Inclusive prefix over the block's NT threads, and the block's sum. sh: NT / 32 entries.
+template <int NT>
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* sh, int64_t& total) {
     constexpr int NW = NT / 32;
-    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0, cost0 = 0;
-    for (int i = tid; i < p.B; i += NT) {
-        const PagedSeq s = paged_seq(p, i);
-        const int64_t c = s.n > 0 ? paged_head_cost<KT>(p, s, TQ) * p.Hkv : 0;
-        if (i == tid) cost0 = c;
-        mine += c;
+    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh[warp] = mine;
-    if (tid == 0) sh[NW] = -1;
+    __syncthreads();  // sh may still be read from the call before
+    if (lane == 31) sh[warp] = v;
     __syncthreads();
-    int64_t W = 0;
-    for (int k = 0; k < NW; ++k) W += sh[k];
-    const int n = int(min(int64_t(gridDim.x), (W + min_tiles - 1) / min_tiles));
-    const int c = int(blockIdx.x);
-    if (c >= n) return n;
-    const int64_t begin = W * c / n;
-    w.left = W * (c + 1) / n - begin;
-    // the request that holds tile `begin`: a running prefix, NT requests at a time
-    int64_t run = 0;
-    for (int a = 0; a < p.B; a += NT) {
-        int64_t cost = cost0;
-        if (a > 0) {
-            cost = 0;
-            if (a + tid < p.B) {
-                const PagedSeq s = paged_seq(p, a + tid);
-                if (s.n > 0) cost = paged_head_cost<KT>(p, s, TQ) * p.Hkv;
-            }
-        }
-        int64_t incl = cost;
+    total = 0;
+    int64_t before = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+    for (int k = 0; k < NW; ++k) {
+        if (k < warp) before += sh[k];
+        total += sh[k];
+    }
+    return v + before;
+}
+
+// Where this CTA's share of the line begins. All threads of the block call it (NT threads, a whole
+// number of warps); every warp leaves with the same walk. False for a CTA without work.
+template <int KT, int OVH, int NT>
+__device__ __forceinline__ bool paged_share(const PagedParams& p, int TQ, int min_cost, int64_t* sh /* [NT / 32 + 2] */,
+                                            PagedWalk<KT, OVH>& w) {
+    constexpr int NW = NT / 32;
+    constexpr int KEEP = 4;  // requests whose cost a thread keeps from the first pass
+    const int tid = int(threadIdx.x), lane = tid & 31;
+    auto cost_of = [&](int i) {
+        if (i >= p.B) return int64_t(0);
+        const PagedSeq s = paged_seq(p, i);
+        return s.n > 0 ? paged_head_cost<KT, OVH>(p, s, TQ) * p.Hkv : int64_t(0);
+    };
+    int64_t kept[KEEP], mine = 0;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+        kept[k] = k * NT < p.B ? cost_of(k * NT + tid) : 0;
+        mine += kept[k];
+    }
+    for (int i = KEEP * NT + tid; i < p.B; i += NT) mine += cost_of(i);
+    int64_t incl = block_prefix<NT>(mine, sh, w.W);
+    w.n = int(min(int64_t(gridDim.x), (w.W + min_cost - 1) / min_cost));
+    const int c = int(blockIdx.x);
+    if (c >= w.n) return false;
+    int64_t begin, end;
+    if (w.W < (int64_t(1) << 31)) {  // 32-bit divisions where they do
+        const uint32_t W = uint32_t(w.W), n = uint32_t(w.n), q = W / n, r = W - q * n;
+        begin = q * uint32_t(c) + r * uint32_t(c) / n;
+        end = q * uint32_t(c + 1) + r * uint32_t(c + 1) / n;
+    } else {
+        begin = w.W * c / w.n;
+        end = w.W * (c + 1) / w.n;
+    }
+    w.left = end - begin;
+    // the request that holds `begin`: a running prefix, NT requests at a time
+    int64_t run = 0;
+    for (int k = 0; k * NT < p.B; ++k) {
+        int64_t cost = mine, total = w.W;
+        if (p.B > NT) {
+            cost = 0;
+            if (k < KEEP) {
+#pragma unroll
+                for (int y = 0; y < KEEP; ++y)
+                    if (y == k) cost = kept[y];
+            } else {
+                cost = cost_of(k * NT + tid);
+            }
+            incl = run + block_prefix<NT>(cost, sh, total);
         }
-        __syncthreads();
-        if (lane == 31) sh[warp] = incl;
-        __syncthreads();
-        int64_t before = run, total = 0;
-        for (int k = 0; k < NW; ++k) {
-            if (k < warp) before += sh[k];
-            total += sh[k];
-        }
-        if (begin >= before + incl - cost && begin < before + incl) {
-            sh[NW] = a + tid;
-            sh[NW + 1] = begin - (before + incl - cost);
+        if (begin >= incl - cost && begin < incl) {
+            sh[NW] = k * NT + tid;
+            sh[NW + 1] = begin - (incl - cost);
         }
         run += total;
         if (begin < run) break;  // the same in all threads
@@ -203,86 +235,109 @@ __device__ __forceinline__ int paged_share(const PagedParams& p, int TQ, int min
     w.s = paged_seq(p, w.i);
     // the head, then the row tile, 32 looked at at a time
     int64_t per_head = 0;
-    for (int t = lane * TQ; t < w.s.n; t += 32 * TQ) {
+    for (int64_t t = int64_t(lane) * TQ; t < w.s.n; t += int64_t(32) * TQ) {
         int first, count;
-        paged_tiles<KT>(p, w.s, t, min(w.s.n, t + TQ), first, count);
-        per_head += count;
+        paged_tiles<KT>(p, w.s, int(t), int(min(int64_t(w.s.n), t + TQ)), first, count);
+        per_head += count + OVH;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, o);
-    w.head = int(rem / per_head);
+    w.head = w.W < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(per_head)) : int(rem / per_head);
     rem -= per_head * w.head;
-    for (int64_t a = 0; a < w.s.n; a += int64_t(32) * TQ) {
-        const int64_t t = a + int64_t(lane) * TQ;
-        int first = 0, count = 0;
-        if (t < w.s.n) paged_tiles<KT>(p, w.s, int(t), int(min(int64_t(w.s.n), t + TQ)), first, count);
-        int64_t incl = count;
+    w.t0 = 0;
+    w.pos = int(rem);
+    if (w.s.n > TQ) {
+        for (int64_t a = 0; a < w.s.n; a += int64_t(32) * TQ) {
+            const int64_t t = a + int64_t(lane) * TQ;
+            int first = 0, count = -OVH;
+            if (t < w.s.n) paged_tiles<KT>(p, w.s, int(t), int(min(int64_t(w.s.n), t + TQ)), first, count);
+            const int64_t cost = count + OVH;
+            int64_t sum = cost;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, rem >= sum - cost && rem < sum);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                w.t0 = int(a) + src * TQ;
+                w.pos = int(rem - __shfl_sync(0xffffffffu, sum - cost, src));
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, sum, 31);
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, rem >= incl - count && rem < incl);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            w.t0 = int(a) + src * TQ;
-            w.off = int(rem - __shfl_sync(0xffffffffu, incl - count, src));
-            break;
-        }
-        rem -= __shfl_sync(0xffffffffu, incl, 31);
     }
     w.unit(p, TQ);
-    return n;
+    return true;
 }
 
-// Joins the pieces of cut units: block (c, y) takes columns [y D / NY, (y + 1) D / NY) of the unit that
-// CTA c - 1 opened and CTA c continues. ROWS is the row pitch of a slot.
-template <int D, int ROWS, int NY>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p, int ctas) {
-    constexpr int COLS = D / NY, V = COLS / 4;  // float4 columns of this block
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = int(blockIdx.x) + 1;
-    const PagedMeta open = p.meta[c - 1];
-    if (!open.opens || !p.meta[c].cont) return;
-    int last = c;
-    while (!p.meta[last].ends && last + 1 < ctas) ++last;
-    // pieces: slot 2 (c - 1) + 1, then slots 2 c, 2 (c + 1), ... 2 last
-    const int pieces = last - c + 2;
-    auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
-    for (int x = int(threadIdx.x); x < open.rows * V; x += 128) {
-        const int r = x / V, col = int(blockIdx.y) * COLS + (x % V) * 4;
-        float m = -INFINITY;
-        for (int i = 0; i < pieces; ++i) m = fmaxf(m, p.part_ml[int64_t(slot(i)) * ROWS + r].x);
-        const float neg = m == -INFINITY ? 0.f : -m;
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < pieces; ++i) {
-            const int64_t at = int64_t(slot(i)) * ROWS + r;
-            const float2 ml = p.part_ml[at];
-            const float4 y = *reinterpret_cast<const float4*>(p.part_o + at * D + col);
-            const float e = ex2(ml.x + neg);  // 2^-inf = 0: a piece that saw no key has l = 0 and O = 0
-            l += e * ml.y;
-            o.x += e * y.x;
-            o.y += e * y.y;
-            o.z += e * y.z;
-            o.w += e * y.w;
+// Orders this kernel behind the one before it in its stream, where it was launched to overlap that one's end.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream start its launch; what it reads of this one it waits for.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Joins the pieces of cut units: grid column c is the unit that CTA c opened, and its block y takes 128
+// groups of four elements of the unit's rows, one to a thread. ROWS is the row pitch of a slot.
+// Bound by latency: pieces are read eight at a time, all loads of the eight in flight together.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
+    grid_wait();
+    const int c = int(blockIdx.x);
+    const PagedMeta u = p.meta[c];
+    const int x = int(blockIdx.y) * 128 + int(threadIdx.x), r = x / (D / 4), col = (x % (D / 4)) * 4;
+    if (u.pieces == 0 || r >= u.rows) return;
+    constexpr int N = 8;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int a = 0; a < u.pieces; a += N) {
+        float2 ml[N];
+        float4 y[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a + k < u.pieces) {
+                const int64_t at = int64_t(a + k == 0 ? 2 * c + 1 : 2 * (c + a + k)) * ROWS + r;
+                ml[k] = p.part_ml[at];
+                y[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+            }
         }
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        const int row = open.row0 + r / p.G, h = open.head * p.G + r % p.G;
-        *reinterpret_cast<uint2*>(p.o + (int64_t(row) * p.H + h) * D + col) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (col == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        float mx = m;
+#pragma unroll
+        for (int k = 0; k < N; ++k) mx = fmaxf(mx, ml[k].x);
+        const float neg = mx == -INFINITY ? 0.f : -mx;
+        const float e0 = ex2(m + neg);  // 2^-inf = 0: nothing so far, or a piece that saw no key
+        m = mx;
+        l *= e0;
+        o.x *= e0;
+        o.y *= e0;
+        o.z *= e0;
+        o.w *= e0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float e = ex2(ml[k].x + neg);
+            l += e * ml[k].y;
+            o.x += e * y[k].x;
+            o.y += e * y[k].y;
+            o.z += e * y[k].z;
+            o.w += e * y[k].w;
+        }
     }
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const int row = u.row0 + r / p.G, h = u.head * p.G + r % p.G;
+    *reinterpret_cast<uint2*>(p.o + (int64_t(row) * p.H + h) * D + col) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (col == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Launches the joining kernel behind the kernel that wrote the pieces, its start overlapped with that
 // kernel's end (it waits for it before its first read).
-template <int D, int ROWS, int NY>
+template <int D, int ROWS>
 inline int launch_paged_join(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (ctas < 2) return ULYSSES_OK;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(ctas - 1), NY);
+    cfg.gridDim = dim3(unsigned(ctas - 1), ROWS * D / 4 / 128);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -290,7 +345,7 @@ inline int launch_paged_join(const PagedParams& p, int ctas, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS, NY>, p, ctas) == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS>, p) == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 
 // Tensor map of a pool's keys or values, (64 elements, token, head, page, 64-element chunk), for copies

@@ -22,7 +22,8 @@ namespace {
 constexpr int kDecodeRows = 16;
 constexpr int kDecodeThreads = 160;
 constexpr int kDecodeMaxCtas = 320;  // 2 per SM, up to 160 SMs: sizes the workspace
-constexpr int kDecodeMinTiles = 2;   // key tiles below which another CTA costs more than it gives
+constexpr int kDecodeMinCost = 2;    // share below which another CTA costs more than it gives
+constexpr int kDecodeUnitCost = 1;   // fixed cost of a unit, in key tiles
 
 template <int D>
 struct DecodeCfg {
@@ -43,7 +44,7 @@ struct DecodeCfg {
     static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-enum : int { TILE_FIRST = 1, TILE_LAST = 2, TILE_MASKED = 4 };
+enum : int { TILE_FIRST = 1, TILE_LAST = 2, TILE_MASKED = 4, TILE_END = 8 };  // END: no tile, the share is done
 
 // One key tile as the producer describes it to the consumers.
 struct DecodeTile {
@@ -94,6 +95,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int* abort_flag = reinterpret_cast<int*>(join + 1);
     auto tile_desc = [&](int st) { return reinterpret_cast<DecodeTile*>(smem + C::OFF_DESC + st * 64); };
 
+    grid_release();
     const int warp = int(warp_id()), lane = int(lane_id());
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -105,12 +107,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         fence_mbar_init();
     }
     const int TQ = kDecodeRows / p.G;
-    PagedWalk<C::KT> w;
-    const int n_ctas = paged_share<C::KT, kDecodeThreads>(p, TQ, kDecodeMinTiles, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    PagedWalk<C::KT, kDecodeUnitCost> w;
     const int cta = int(blockIdx.x);
+    const bool work = paged_share<C::KT, kDecodeUnitCost, kDecodeThreads>(p, TQ, kDecodeMinCost,
+                                                                          reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     __syncthreads();
-    if (cta >= n_ctas) {
-        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0, 0, 0};
+    if (!work) {
+        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0};
         return;
     }
     const Abort ab{abort_flag, p.err, KID_PAGED};
@@ -127,83 +130,81 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int key = key0 + my_row;
             return lane < copies && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
         };
-        PagedMeta meta{0, 0, 0, 0, 0, 0};
-        int issued = 0, used[C::STAGES] = {};
+        PagedMeta meta{0, 0, 0, 0};
+        int issued = 0;
         bool ok = true, first_piece = true;
-        bool fresh = true;  // the next tile is the piece's first
-        bool whole = false; // the piece begins its unit
-        int id = lookup((w.first + w.off) * C::KT);
-        while (w.left > 0) {
-            const int st = issued % C::STAGES;
-            const int key0 = (w.first + w.off) * C::KT;
-            const bool last = w.off + 1 == w.count || w.left == 1;
-            if (fresh) whole = w.off == 0;
-            int slot = -1;
-            if (last) {
-                const bool ends = w.off + 1 == w.count;
-                if (first_piece && !whole) {
+        auto free_stage = [&](int st) {
+            if (issued >= C::STAGES)
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + st, ((issued / C::STAGES) - 1) & 1, ab, ROLE_LOAD, 1));
+            return ok;
+        };
+        while (ok && w.left > 0) {
+            int off, tiles;
+            w.take(off, tiles);
+            if (tiles > 0) {
+                int slot = -1;
+                const bool ends = off + tiles == w.count;
+                if (first_piece && off > 0) {
                     slot = 2 * cta;
-                    meta.cont = 1;
-                    meta.ends = ends;
                 } else if (!ends) {
                     slot = 2 * cta + 1;
-                    meta.opens = 1;
-                    meta.head = w.head;
-                    meta.row0 = w.s.start + w.t0;
-                    meta.rows = (w.t1 - w.t0) * p.G;
+                    meta = PagedMeta{w.pieces(cta), w.head, w.s.start + w.t0, (w.t1 - w.t0) * p.G};
+                }
+                first_piece = false;
+                const int rows = (w.t1 - w.t0) * p.G;
+                int id = lookup((w.first + off) * C::KT);
+                for (int x = 0; x < tiles; ++x) {
+                    const int st = issued % C::STAGES;
+                    const int key0 = (w.first + off + x) * C::KT;
+                    const int id_next = x + 1 < tiles ? lookup(key0 + C::KT) : -1;
+                    if (!free_stage(st)) break;
+                    const bool good = unsigned(id) < unsigned(p.num_pages);
+                    // one bit per copy (the K copy of each page), spread to 16 keys a bit
+                    const unsigned pages = __ballot_sync(0xffffffffu, good && (lane & 1) == 0);
+                    const int page_of = (min(lane, C::KT / 16 - 1) * 16) >> log_rows;  // of keys [16 lane, 16 lane + 16)
+                    const uint32_t valid = __ballot_sync(0xffffffffu, lane < C::KT / 16 && ((pages >> (2 * page_of)) & 1u));
+                    uint8_t* stage = smem + st * C::STAGE_BYTES;
+                    if (lane == 0) {
+                        DecodeTile t;
+                        const int pos0 = w.s.base + w.t0, pos1 = w.s.base + w.t1 - 1;  // of the first and last row
+                        const bool clear = valid == (1u << (C::KT / 16)) - 1 && key0 + C::KT <= w.s.kv &&
+                                           (!p.causal || (key0 + C::KT <= pos0 + 1 && (p.window == 0 || key0 > pos1 - p.window)));
+                        t.flags = (x == 0 ? TILE_FIRST : 0) | (x + 1 == tiles ? TILE_LAST : 0) | (clear ? 0 : TILE_MASKED);
+                        t.key0 = key0; t.kv = w.s.kv; t.base = pos0;
+                        t.rows = rows; t.row0 = w.s.start + w.t0; t.head = w.head; t.slot = slot;
+                        t.valid = valid;
+                        *tile_desc(st) = t;
+                        mbar_arrive_expect_tx(full + st, C::STAGE_BYTES + (x == 0 ? rows * D * 2 : 0));
+                    }
+                    __syncwarp();
+                    if (lane < copies) {
+                        // a page that does not exist is copied from behind the pool: zeros
+                        const int page = good ? id : p.num_pages, row = (key0 + my_row) & ((1 << p.page_shift) - 1);
+                        tma_load_5d(stage + (lane & 1) * C::KV_BYTES + my_row * (D * 2), (lane & 1) ? &tm_v : &tm_k, full + st, 0,
+                                    row, w.head, page, 0);
+                    }
+                    if (x == 0 && lane < rows) {
+                        const __nv_bfloat16* src = p.q + int64_t(w.s.start + w.t0 + lane / p.G) * p.q_stride +
+                                                   int64_t(w.head * p.G + lane % p.G) * D;
+                        bulk_load(smem + C::OFF_Q + st * C::Q_BYTES + lane * C::Q_PITCH, src, D * 2, full + st);
+                    }
+                    ++issued;
+                    id = id_next;
                 }
             }
-            if (issued >= C::STAGES) {
-                ok = mbar_wait(empty + st, ((issued / C::STAGES) - 1) & 1, ab, ROLE_LOAD, 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-            const bool good = unsigned(id) < unsigned(p.num_pages);
-            // one bit per copy (the K copy of each page), spread to 16 keys a bit
-            const unsigned pages = __ballot_sync(0xffffffffu, good && (lane & 1) == 0);
-            const int page_of = (lane * 16) >> log_rows;  // of keys [16 lane, 16 lane + 16)
-            const uint32_t valid = __ballot_sync(0xffffffffu, lane < C::KT / 16 && ((pages >> (2 * page_of)) & 1u));
-            const int rows = (w.t1 - w.t0) * p.G;
-            uint8_t* stage = smem + st * C::STAGE_BYTES;
-            if (lane == 0) {
-                DecodeTile t;
-                const int pos0 = w.s.base + w.t0, pos1 = w.s.base + w.t1 - 1;  // of the first and last row
-                const bool clear = valid == (1u << (C::KT / 16)) - 1 && key0 + C::KT <= w.s.kv &&
-                                   (!p.causal || (key0 + C::KT <= pos0 + 1 && (p.window == 0 || key0 > pos1 - p.window)));
-                t.flags = (fresh ? TILE_FIRST : 0) | (last ? TILE_LAST : 0) | (clear ? 0 : TILE_MASKED);
-                t.key0 = key0; t.kv = w.s.kv; t.base = pos0;
-                t.rows = rows; t.row0 = w.s.start + w.t0; t.head = w.head; t.slot = slot;
-                t.valid = valid;
-                *tile_desc(st) = t;
-                mbar_arrive_expect_tx(full + st, C::STAGE_BYTES + (fresh ? rows * D * 2 : 0));
-            }
-            __syncwarp();
-            if (lane < copies) {
-                // a page that does not exist is copied from behind the pool: zeros
-                const int page = good ? id : p.num_pages, row = (key0 + my_row) & ((1 << p.page_shift) - 1);
-                tma_load_5d(stage + (lane & 1) * C::KV_BYTES + my_row * (D * 2), (lane & 1) ? &tm_v : &tm_k, full + st, 0, row,
-                            w.head, page, 0);
-            }
-            if (fresh && lane < rows) {
-                const __nv_bfloat16* src = p.q + int64_t(w.s.start + w.t0 + lane / p.G) * p.q_stride +
-                                           int64_t(w.head * p.G + lane % p.G) * D;
-                bulk_load(smem + C::OFF_Q + st * C::Q_BYTES + lane * C::Q_PITCH, src, D * 2, full + st);
-            }
-            used[st] = issued / C::STAGES + 1;
-            ++issued;
-            --w.left;
-            fresh = last;
-            if (last) first_piece = false;
-            if (w.left > 0) {
-                if (w.off + 1 < w.count) ++w.off;
-                else w.next_unit(p, TQ);
-                id = lookup((w.first + w.off) * C::KT);
-            }
+            if (ok && w.left > 0) w.next_unit(p, TQ);
         }
         if (lane == 0) p.meta[cta] = meta;
-        if (!ok && lane == 0)
+        if (ok && free_stage(issued % C::STAGES)) {
+            if (lane == 0) {
+                tile_desc(issued % C::STAGES)->flags = TILE_END;
+                mbar_arrive(full + issued % C::STAGES);
+            }
+        } else if (lane == 0) {
+            // copies already in flight land before the CTA can exit
             for (int s = 0; s < C::STAGES; ++s)
-                if (used[s] > 0) mbar_drain(full + s, (used[s] - 1) & 1);
+                if (issued > s) mbar_drain(full + s, ((issued - 1 - s) / C::STAGES) & 1);
+        }
     } else {
         // ------------------------------------------------------------------ consumers
         const int cw = warp - 1;
@@ -216,10 +217,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int r0 = lane >> 2, r1 = r0 + 8;
         for (int it = 0;; ++it) {
             const int st = it % C::STAGES;
-            // the share's length is the same in every warp
-            if (it >= w.left) break;
             if (!__all_sync(0xffffffffu, mbar_wait(full + st, (it / C::STAGES) & 1, ab, ROLE_SOFTMAX, 1))) break;
             const DecodeTile t = *tile_desc(st);
+            if (t.flags & TILE_END) break;
             const uint32_t sK = smem_u32(smem + st * C::STAGE_BYTES), sV = sK + C::KV_BYTES;
             if (t.flags & TILE_FIRST) {
                 const uint32_t sQ = smem_u32(smem + C::OFF_Q + st * C::Q_BYTES);
@@ -409,7 +409,7 @@ int launch_decode_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cuda
     p.meta = reinterpret_cast<PagedMeta*>(ws);
     kern<<<ctas, kDecodeThreads, C::SMEM_BYTES, stream>>>(mk, mv, p, __builtin_ctz(unsigned(rows)));
     if (cudaGetLastError() != cudaSuccess) return ULYSSES_ERR_CUDA;
-    return launch_paged_join<D, kDecodeRows, 4>(p, ctas, stream);
+    return launch_paged_join<D, kDecodeRows>(p, ctas, stream);
 }
 
 }  // namespace
