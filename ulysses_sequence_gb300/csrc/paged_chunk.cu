@@ -350,51 +350,46 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t what = info[j % kInfoRing];
                 const bool masked = what & kInfoMasked;
                 const int key0 = u.key0 + i * kTile;
-                auto mask_half = [&](float* v, int c0) {
-                    if (masked) {
-                        const int h = hi - key0 - c0, b = lo - key0 - c0;
-                        const uint32_t pages = what >> (c0 / 16);
+                // all 128 scores of the row at once in registers: one trip through TMEM, four independent
+                // chains for the maximum and the sum
+                float v[128];
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (x >= h || x < b || !((pages >> (x / 16)) & 1u)) v[x] = -INFINITY;
-                    }
-                };
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
-                    float v[64];
-                    tmem_ld32(tS + hh * 64, v);
-                    tmem_ld32(tS + hh * 64 + 32, v + 32);
-                    tmem_wait_ld();
-                    mask_half(v, hh * 64);
+                for (int x = 0; x < 4; ++x) tmem_ld32(tS + x * 32, v + x * 32);
+                tmem_wait_ld();
+                if (masked) {
+                    const int h = hi - key0, b = lo - key0;
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) mx = fmaxf(mx, v[x]);
+                    for (int x = 0; x < 128; ++x)
+                        if (x >= h || x < b || !((what >> (x / 16)) & 1u)) v[x] = -INFINITY;
                 }
+                float mx4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int x = 4; x < 128; ++x) mx4[x & 3] = fmaxf(mx4[x & 3], v[x]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 const float m_new = fmaxf(m_used, mx * p.scale_log2);
                 const bool need = valid && m_new > m_used + 8.0f;
                 const float alpha = need ? ex2(m_used - m_new) : 1.0f;  // ex2(-inf) = 0 for a first maximum
                 if (need) m_used = m_new;
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                // the weights, rounded to bf16 for the matrix product (their sum is not), over the scores:
-                // half hh lands in columns [32 hh, 32 hh + 32), already read
-                float rs = 0.f;
-#pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
-                    float v[64];
-                    tmem_ld32(tS + hh * 64, v);
-                    tmem_ld32(tS + hh * 64 + 32, v + 32);
-                    tmem_wait_ld();
-                    mask_half(v, hh * 64);
+                // the weights, rounded to bf16 for the matrix product (their sum is not), over the scores' first
+                // 64 columns, all read by now
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
+                float2 rs4[4] = {};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
-                        const float e0 = ex2(fmaf(v[2 * x], p.scale_log2, neg_m));
-                        const float e1 = ex2(fmaf(v[2 * x + 1], p.scale_log2, neg_m));
-                        rs += e0 + e1;
-                        pk[x] = pack_bf16(e0, e1);
+                        float2 e = fma2(make_float2(v[64 * g + 2 * x], v[64 * g + 2 * x + 1]), sc2, nm2);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        rs4[x & 3] = add2(rs4[x & 3], e);
+                        pk[x] = pack_bf16(e.x, e.y);
                     }
-                    tmem_st32_u(tS + hh * 32, pk);
+                    tmem_st32_u(tS + g * 32, pk);
                 }
+                rs4[0] = add2(add2(rs4[0], rs4[1]), add2(rs4[2], rs4[3]));
+                const float rs = rs4[0].x + rs4[0].y;
                 l_sum = l_sum * alpha + rs;
                 if (i > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
@@ -436,6 +431,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int unit_row = t * TOK * p.G + row;
             const int q_row = u.row0 + t * TOK + tok, h = u.head * p.G + row % p.G;
             __nv_bfloat16* dst = p.o + (int64_t(q_row) * p.H + h) * D;
+            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // o may be 16-byte aligned only
             float* part = p.part_o + (int64_t(max(u.slot, 0)) * kChunkRows + unit_row) * D;
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
@@ -447,14 +443,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int y = 0; y < 32; ++y) o[y] *= inv;
                 if (u.slot >= 0) {
 #pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        reinterpret_cast<float4*>(part + x * 32)[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    for (int y = 0; y < 4; ++y) st_global_v8(part + x * 32 + y * 8, reinterpret_cast<const uint32_t*>(o + 8 * y));
                 } else {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        reinterpret_cast<uint4*>(dst + x * 32)[y] =
-                            make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
-                                       pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7]));
+                    for (int y = 0; y < 16; ++y) pk[y] = pack_bf16(o[2 * y], o[2 * y + 1]);
+                    if (wide) {
+                        st_global_v8(dst + x * 32, pk);
+                        st_global_v8(dst + x * 32 + 16, pk + 8);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            reinterpret_cast<uint4*>(dst + x * 32)[y] = make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+                    }
                 }
             }
             if (valid) {
