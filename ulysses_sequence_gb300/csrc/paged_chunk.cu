@@ -328,28 +328,30 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int piece = 0; ok; ++piece) {
             ok = __all_sync(0xffffffffu, mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
             if (!ok) break;
-            const ChunkPiece u = pieces[piece & 1];
-            if (u.tiles == 0) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(piece_empty + (piece & 1));
-            const int my_tokens = min(TOK, u.tokens - t * TOK);
-            if (my_tokens <= 0) {  // the unit has one tile
-                j += u.tiles;
+            // read again where needed: registers are short in the loop below
+            const volatile ChunkPiece& u = pieces[piece & 1];
+            const int tiles = u.tiles;
+            if (tiles == 0) break;
+            auto done_with_piece = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(piece_empty + (piece & 1));
+            };
+            const bool valid = tok < u.tokens - t * TOK && tok < TOK;
+            if (u.tokens <= t * TOK) {  // the unit has one tile
+                done_with_piece();
+                j += tiles;
                 continue;
             }
-            const bool valid = tok < my_tokens;
-            const int pos = u.pos + t * TOK + tok;
-            const int hi = p.causal ? max(0, min(u.kv, pos + 1)) : u.kv;     // the row sees keys [lo, hi)
-            const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            const int kv = u.kv;
+            int key0 = u.key0;
             float m_used = -INFINITY, l_sum = 0.f;  // running maximum (log2 domain) and sum
-            for (int i = 0; i < u.tiles; ++i, ++j) {
+            for (int i = 0; i < tiles; ++i, ++j, key0 += kTile) {
                 ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, cs++ & 1, ab, ROLE_SOFTMAX, 2) &&
                                                  mbar_wait(info_full + j % kInfoRing, (j / kInfoRing) & 1, ab, ROLE_SOFTMAX, 3));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t what = info[j % kInfoRing];
                 const bool masked = what & kInfoMasked;
-                const int key0 = u.key0 + i * kTile;
                 // all 128 scores of the row at once in registers: one trip through TMEM, four independent
                 // chains for the maximum and the sum
                 float v[128];
@@ -357,6 +359,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int x = 0; x < 4; ++x) tmem_ld32(tS + x * 32, v + x * 32);
                 tmem_wait_ld();
                 if (masked) {
+                    // the row sees keys [lo, hi)
+                    const int pos = u.pos + t * TOK + tok;
+                    const int hi = p.causal ? max(0, min(kv, pos + 1)) : kv, lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
                     const int h = hi - key0, b = lo - key0;
 #pragma unroll
                     for (int x = 0; x < 128; ++x)
@@ -376,17 +381,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
                 float2 rs4[4] = {};
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pk[32];
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        float2 e = fma2(make_float2(v[64 * g + 2 * x], v[64 * g + 2 * x + 1]), sc2, nm2);
+                    for (int x = 0; x < 16; ++x) {
+                        float2 e = fma2(make_float2(v[32 * g + 2 * x], v[32 * g + 2 * x + 1]), sc2, nm2);
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         rs4[x & 3] = add2(rs4[x & 3], e);
                         pk[x] = pack_bf16(e.x, e.y);
                     }
-                    tmem_st32_u(tS + g * 32, pk);
+                    tmem_st16_u(tS + g * 16, pk);
                 }
                 rs4[0] = add2(add2(rs4[0], rs4[1]), add2(rs4[2], rs4[3]));
                 const float rs = rs4[0].x + rs4[0].y;
@@ -402,12 +407,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tmem_st32(tO + x * 32, o);
                     }
                 }
-                if (t == 0 && key0 + kTile > u.kv) {
+                if (t == 0 && key0 + kTile > kv) {
                     // clear the values behind the last key; tile 1's product follows tile 0's
                     const int sv = j % NSV;
                     ok = __all_sync(0xffffffffu, mbar_wait(v_full + sv, (j / NSV) & 1, ab, ROLE_SOFTMAX, 4));
                     if (!ok) break;
-                    if (key0 + row >= u.kv) {
+                    if (key0 + row >= kv) {
                         const uint32_t a = smem_u32(sV + sv * C::TILE_BYTES) + row * 128;
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
@@ -427,12 +432,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             tc_fence_after();
             const bool any_key = l_sum > 0.f;
-            const float inv = u.slot >= 0 ? 1.0f : (any_key ? 1.0f / l_sum : 0.f);
+            const int slot = u.slot;
+            const float inv = slot >= 0 ? 1.0f : (any_key ? 1.0f / l_sum : 0.f);
             const int unit_row = t * TOK * p.G + row;
             const int q_row = u.row0 + t * TOK + tok, h = u.head * p.G + row % p.G;
             __nv_bfloat16* dst = p.o + (int64_t(q_row) * p.H + h) * D;
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // o may be 16-byte aligned only
-            float* part = p.part_o + (int64_t(max(u.slot, 0)) * kChunkRows + unit_row) * D;
+            float* part = p.part_o + (int64_t(max(slot, 0)) * kChunkRows + unit_row) * D;
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
                 float o[32];
@@ -441,7 +447,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!valid) continue;
 #pragma unroll
                 for (int y = 0; y < 32; ++y) o[y] *= inv;
-                if (u.slot >= 0) {
+                if (slot >= 0) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y) st_global_v8(part + x * 32 + y * 8, reinterpret_cast<const uint32_t*>(o + 8 * y));
                 } else {
@@ -459,9 +465,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             if (valid) {
-                if (u.slot >= 0) p.part_ml[int64_t(u.slot) * kChunkRows + unit_row] = make_float2(m_used, l_sum);
+                if (slot >= 0) p.part_ml[int64_t(slot) * kChunkRows + unit_row] = make_float2(m_used, l_sum);
                 else p.lse[int64_t(h) * p.T + q_row] = any_key ? (m_used + log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
             }
+            done_with_piece();
             tc_fence_before();
         }
     }
