@@ -3,6 +3,8 @@
 // the device only, so a call launches both, each passing over the other's requests, unless the
 // caller's bound on new tokens says that the decode kernel's are all (it then takes every request,
 // however long: the bound chooses, it does not decide what is computed) or the group is too wide for it.
+#include <algorithm>
+
 #include "paged_common.cuh"
 
 namespace ulysses {
@@ -22,10 +24,21 @@ bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* bas
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr);
 }
 
+template <int D>
+static int launch_join(const PagedParams& p, const PagedParts& decode, const PagedParts& chunk, cudaStream_t stream) {
+    const int64_t blocks = int64_t(std::max(decode.ctas - 1, 0)) * (decode.rows * D / 512) +
+                           int64_t(std::max(chunk.ctas - 1, 0)) * (chunk.rows * D / 512);
+    if (blocks == 0) return ULYSSES_OK;
+    return launch_chained(paged_join_kernel<D>, dim3(unsigned(blocks)), 128, 0, stream, p, decode, chunk) ? ULYSSES_OK
+                                                                                                         : ULYSSES_ERR_CUDA;
+}
+
 size_t paged_attn_workspace_bytes(int H, int H_kv, int d_h, int max_q) {
     const int G = H / H_kv;
-    return (decode_fits(G) ? paged_decode_workspace_bytes(d_h) : 0) +
-           (decode_only(G, max_q) ? 0 : paged_chunk_workspace_bytes(d_h));
+    size_t decode = 0, chunk = 0;
+    if (decode_fits(G)) paged_decode_parts(nullptr, d_h, &decode);
+    if (!decode_only(G, max_q)) paged_chunk_parts(nullptr, d_h, &chunk);
+    return decode + chunk;
 }
 
 int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -43,17 +56,25 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.err = device_error_word();
     if (!p.err) return ULYSSES_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const int d = a.cache.d_h;
     const bool only = decode_only(p.G, a.max_q);
+    PagedParts decode{}, chunk{};
+    size_t bytes = 0;
     p.min_rows = 1;
     if (decode_fits(p.G)) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
-        const int rc = launch_paged_decode(a, p, ws, stream);
-        if (rc != ULYSSES_OK || only) return rc;
+        p.parts = decode = paged_decode_parts(ws, d, &bytes);
+        const int rc = launch_paged_decode(a, p, stream);
+        if (rc != ULYSSES_OK) return rc;
         p.min_rows = paged_decode_rows() + 1;
-        ws += paged_decode_workspace_bytes(a.cache.d_h);
     }
-    p.max_rows = 0x7fffffff;
-    return launch_paged_chunk(a, p, ws, stream);
+    if (!only) {
+        p.max_rows = 0x7fffffff;
+        p.parts = chunk = paged_chunk_parts(ws + bytes, d, &bytes);
+        const int rc = launch_paged_chunk(a, p, decode_fits(p.G), stream);
+        if (rc != ULYSSES_OK) return rc;
+    }
+    return d == 128 ? launch_join<128>(p, decode, chunk, stream) : launch_join<64>(p, decode, chunk, stream);
 }
 
 }  // namespace ulysses

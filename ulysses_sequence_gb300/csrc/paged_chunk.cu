@@ -33,7 +33,7 @@ constexpr int kChunkThreads = 320;
 constexpr int kChunkRows = 2 * kTile;
 constexpr int kChunkMaxCtas = 160;   // one per SM: sizes the workspace
 constexpr int kChunkMinCost = 4;     // share below which another CTA costs more than it gives
-constexpr int kChunkUnitCost = 2;    // fixed cost of a unit, in key tiles
+constexpr int kChunkUnitCost = 3;    // fixed cost of a unit, in key tiles
 constexpr int kInfoRing = 8;         // tiles that the producer may describe ahead (it leads by at most 7)
 
 template <int D>
@@ -65,10 +65,14 @@ static_assert(2 * sizeof(ChunkPiece) <= 128, "piece ring");
 
 constexpr uint32_t kInfoMasked = 0x100;  // some row does not see all of the tile; bits 0-7: pages of 16 keys that exist
 
+// behind_decode: launched behind the decode kernel of the same call, with which it shares inputs but no
+// output: its CTAs take the SMs as that kernel's leave them, and wait for it only before they end, so that
+// what follows finds both done. The inputs are complete: the decode kernel waited for them before it
+// released this one.
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const PagedParams p, int log_rows /* of one page copy */) {
+                   const __grid_constant__ CUtensorMap tm_v, const PagedParams p, int log_rows /* of one page copy */, int behind_decode) {
     using C = ChunkCfg<D>;
     constexpr int NSK = C::NSK, NSV = C::NSV;
     extern __shared__ uint8_t smem_raw[];
@@ -118,13 +122,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fence_mbar_init();
     }
     const int TOK = kTile / p.G, TQ = 2 * TOK;  // tokens of a tile, of a unit
+    if (!behind_decode) grid_wait();
     PagedWalk<kTile, kChunkUnitCost> w;
     const int cta = int(blockIdx.x);
     const bool work = paged_share<kTile, kChunkUnitCost, kChunkThreads>(p, TQ, kChunkMinCost,
                                                                         reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     __syncthreads();
     if (!work) {
-        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0};
+        if (threadIdx.x == 0) p.parts.meta[cta] = PagedMeta{0, 0, 0, 0};
+        if (behind_decode) grid_wait();
         return;
     }
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -233,7 +239,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_arrive(piece_full + (piece & 1));
         }
         if (lane == 0) {
-            p.meta[cta] = meta;
+            p.parts.meta[cta] = meta;
             if (!ok) {
                 // copies already in flight land before the CTA can exit
                 if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
@@ -438,7 +444,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int q_row = u.row0 + t * TOK + tok, h = u.head * p.G + row % p.G;
             __nv_bfloat16* dst = p.o + (int64_t(q_row) * p.H + h) * D;
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // o may be 16-byte aligned only
-            float* part = p.part_o + (int64_t(max(slot, 0)) * kChunkRows + unit_row) * D;
+            float* part = p.parts.o + (int64_t(max(slot, 0)) * kChunkRows + unit_row) * D;
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
                 float o[32];
@@ -465,7 +471,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             if (valid) {
-                if (slot >= 0) p.part_ml[int64_t(slot) * kChunkRows + unit_row] = make_float2(m_used, l_sum);
+                if (slot >= 0) p.parts.ml[int64_t(slot) * kChunkRows + unit_row] = make_float2(m_used, l_sum);
                 else p.lse[int64_t(h) * p.T + q_row] = any_key ? (m_used + log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
             }
             done_with_piece();
@@ -479,10 +485,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
+    if (behind_decode) grid_wait();
 }
 
 template <int D>
-int launch_chunk_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaStream_t stream) {
+int launch_chunk_d(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream) {
     using C = ChunkCfg<D>;
     const int rows = std::min(a.cache.page_size, kTile);
     const int chunks = rows == kTile ? D / 64 : 1;
@@ -499,27 +506,20 @@ int launch_chunk_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaS
         return ULYSSES_ERR_CUDA;
     auto kern = paged_chunk_kernel<D>;
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ULYSSES_ERR_CUDA;
-    const int ctas = std::min(device_sm_count(), kChunkMaxCtas);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.part_o = reinterpret_cast<float*>(ws);
-    ws += size_t(2) * kChunkMaxCtas * kChunkRows * D * 4;
-    p.part_ml = reinterpret_cast<float2*>(ws);
-    ws += size_t(2) * kChunkMaxCtas * kChunkRows * 8;
-    p.meta = reinterpret_cast<PagedMeta*>(ws);
-    kern<<<ctas, kChunkThreads, C::SMEM_BYTES, stream>>>(mq, mk, mv, p, __builtin_ctz(unsigned(rows)));
-    if (cudaGetLastError() != cudaSuccess) return ULYSSES_ERR_CUDA;
-    return launch_paged_join<D, kChunkRows>(p, ctas, stream);
+    if (!launch_chained(kern, dim3(unsigned(p.parts.ctas)), kChunkThreads, C::SMEM_BYTES, stream, mq, mk, mv, p,
+                        __builtin_ctz(unsigned(rows)), int(behind_decode)))
+        return ULYSSES_ERR_CUDA;
+    return ULYSSES_OK;
 }
 
 }  // namespace
 
-size_t paged_chunk_workspace_bytes(int d_h) {
-    const size_t n = size_t(2) * kChunkMaxCtas * kChunkRows * (size_t(d_h) * 4 + 8) + kChunkMaxCtas * sizeof(PagedMeta);
-    return (n + 255) / 256 * 256;
+PagedParts paged_chunk_parts(void* workspace, int d_h, size_t* bytes) {
+    return paged_parts(workspace, kChunkMaxCtas, std::min(device_sm_count(), kChunkMaxCtas), kChunkRows, d_h, bytes);
 }
 
-int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream) {
-    return a.cache.d_h == 128 ? launch_chunk_d<128>(a, p, workspace, stream) : launch_chunk_d<64>(a, p, workspace, stream);
+int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream) {
+    return a.cache.d_h == 128 ? launch_chunk_d<128>(a, p, behind_decode, stream) : launch_chunk_d<64>(a, p, behind_decode, stream);
 }
 
 }  // namespace ulysses

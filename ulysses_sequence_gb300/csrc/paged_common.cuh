@@ -16,6 +16,22 @@
 
 namespace ulysses {
 
+// What the joining kernel knows of CTA c: the unit that its last piece opens and later CTAs go on with. The
+// opening piece is in slot 2 c + 1, those of CTAs c + 1, ... in slots 2 (c + 1), ...
+struct PagedMeta {
+    int pieces;  // of the unit, 0 where there is none
+    int head, row0, rows;
+};
+
+// The pieces that one kernel's CTAs leave, in the workspace.
+struct PagedParts {
+    float* o;         // [2 * CTAs][rows][d] fp32, not normalised
+    float2* ml;       // [2 * CTAs][rows] (m in the log2 domain, l)
+    PagedMeta* meta;  // [CTAs]
+    int rows;         // pitch of a slot: the rows of a unit
+    int ctas;         // of the launch; 0 where the kernel is not launched
+};
+
 struct PagedParams {
     int B, T, H, Hkv, G;
     int max_pages, num_pages, page_shift;
@@ -28,17 +44,8 @@ struct PagedParams {
     const int32_t *cu_q, *kv_lens, *table;
     __nv_bfloat16* o;
     float* lse;
-    float* part_o;           // [2 * CTAs][rows][d] fp32 pieces of cut units, not normalised
-    float2* part_ml;         // [2 * CTAs][rows] (m in the log2 domain, l)
-    struct PagedMeta* meta;  // [CTAs]
+    PagedParts parts;        // of the kernel that gets these parameters
     uint32_t* err;
-};
-
-// What the joining kernel knows of CTA c: the unit that its last piece opens and later CTAs go on with. The
-// opening piece is in slot 2 c + 1, those of CTAs c + 1, ... in slots 2 (c + 1), ...
-struct PagedMeta {
-    int pieces;  // of the unit, 0 where there is none
-    int head, row0, rows;
 };
 
 // The new rows [start, start + n) of request i, its keys [0, kv), and the position of row 0.
@@ -272,20 +279,20 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, int TQ, int mi
     return true;
 }
 
-// Orders this kernel behind the one before it in its stream, where it was launched to overlap that one's end.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel of the stream start its launch; what it reads of this one it waits for.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// Joins the pieces of cut units: grid column c is the unit that CTA c opened, and its block y takes 128
-// groups of four elements of the unit's rows, one to a thread. ROWS is the row pitch of a slot.
-// Bound by latency: pieces are read eight at a time, all loads of the eight in flight together.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
+// Joins the pieces of cut units of both kernels of a call: a unit's rows are cut into blocks of 128 groups
+// of four elements, one to a thread; the blocks of the units that the CTAs of `a` opened come first, then
+// those of `b`. Bound by latency: pieces are read eight at a time, all loads of the eight in flight together.
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p, const PagedParts a_parts, const PagedParts b_parts) {
+    const int a_blocks = a_parts.ctas > 0 ? (a_parts.ctas - 1) * (a_parts.rows * D / 512) : 0;
+    const bool second = int(blockIdx.x) >= a_blocks;
+    const PagedParts& w = second ? b_parts : a_parts;
+    const int block = int(blockIdx.x) - (second ? a_blocks : 0), per = w.rows * D / 512;
+    const int c = block / per;
+    const int x = (block - c * per) * 128 + int(threadIdx.x), r = x / (D / 4), col = (x % (D / 4)) * 4;
     grid_wait();
-    const int c = int(blockIdx.x);
-    const PagedMeta u = p.meta[c];
-    const int x = int(blockIdx.y) * 128 + int(threadIdx.x), r = x / (D / 4), col = (x % (D / 4)) * 4;
+    grid_release();
+    const PagedMeta u = w.meta[c];
     if (u.pieces == 0 || r >= u.rows) return;
     constexpr int N = 8;
     float m = -INFINITY, l = 0.f;
@@ -298,9 +305,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
             ml[k] = make_float2(-INFINITY, 0.f);
             y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (a + k < u.pieces) {
-                const int64_t at = int64_t(a + k == 0 ? 2 * c + 1 : 2 * (c + a + k)) * ROWS + r;
-                ml[k] = p.part_ml[at];
-                y[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + col);
+                const int64_t at = int64_t(a + k == 0 ? 2 * c + 1 : 2 * (c + a + k)) * w.rows + r;
+                ml[k] = w.ml[at];
+                y[k] = *reinterpret_cast<const float4*>(w.o + at * D + col);
             }
         }
         float mx = m;
@@ -331,32 +338,32 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
     if (col == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Launches the joining kernel behind the kernel that wrote the pieces, its start overlapped with that
-// kernel's end (it waits for it before its first read).
-template <int D, int ROWS>
-inline int launch_paged_join(const PagedParams& p, int ctas, cudaStream_t stream) {
-    if (ctas < 2) return ULYSSES_OK;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(ctas - 1), ROWS * D / 4 / 128);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS>, p) == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
-}
-
 // Tensor map of a pool's keys or values, (64 elements, token, head, page, 64-element chunk), for copies
 // of `rows` tokens of one page and head by `chunks` chunks (chunk after chunk), 128-byte swizzle.
 bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks);
 
-// Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu).
+// Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu). p.parts is filled in; the
+// workspace sizes are those of each kernel's pieces.
 int paged_decode_rows();
-size_t paged_decode_workspace_bytes(int d_h);
-int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream);
-size_t paged_chunk_workspace_bytes(int d_h);
-int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream);
+PagedParts paged_decode_parts(void* workspace, int d_h, size_t* bytes);
+PagedParts paged_chunk_parts(void* workspace, int d_h, size_t* bytes);
+int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
+int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream);
+
+// Pieces of `most` CTAs at the front of a workspace, for a launch of `ctas` of them.
+inline PagedParts paged_parts(void* workspace, int most, int ctas, int rows, int d_h, size_t* bytes) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PagedParts w{};
+    w.o = reinterpret_cast<float*>(ws);
+    size_t at = size_t(2) * most * rows * d_h * 4;
+    w.ml = reinterpret_cast<float2*>(ws + at);
+    at += size_t(2) * most * rows * 8;
+    w.meta = reinterpret_cast<PagedMeta*>(ws + at);
+    at += size_t(most) * sizeof(PagedMeta);
+    w.rows = rows;
+    w.ctas = ctas;
+    *bytes = (at + 255) / 256 * 256;
+    return w;
+}
 
 }  // namespace ulysses

@@ -95,7 +95,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int* abort_flag = reinterpret_cast<int*>(join + 1);
     auto tile_desc = [&](int st) { return reinterpret_cast<DecodeTile*>(smem + C::OFF_DESC + st * 64); };
 
-    grid_release();
     const int warp = int(warp_id()), lane = int(lane_id());
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -107,13 +106,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         fence_mbar_init();
     }
     const int TQ = kDecodeRows / p.G;
+    grid_wait();
+    grid_release();  // not before the wait: the chunk kernel starts behind this without one
     PagedWalk<C::KT, kDecodeUnitCost> w;
     const int cta = int(blockIdx.x);
     const bool work = paged_share<C::KT, kDecodeUnitCost, kDecodeThreads>(p, TQ, kDecodeMinCost,
                                                                           reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     __syncthreads();
     if (!work) {
-        if (threadIdx.x == 0) p.meta[cta] = PagedMeta{0, 0, 0, 0};
+        if (threadIdx.x == 0) p.parts.meta[cta] = PagedMeta{0, 0, 0, 0};
         return;
     }
     const Abort ab{abort_flag, p.err, KID_PAGED};
@@ -194,7 +195,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             if (ok && w.left > 0) w.next_unit(p, TQ);
         }
-        if (lane == 0) p.meta[cta] = meta;
+        if (lane == 0) p.parts.meta[cta] = meta;
         if (ok && free_stage(issued % C::STAGES)) {
             if (lane == 0) {
                 tile_desc(issued % C::STAGES)->flags = TILE_END;
@@ -370,8 +371,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     }
                     if (t.slot >= 0) {
                         const int64_t row = int64_t(t.slot) * kDecodeRows + r;
-                        *reinterpret_cast<float4*>(p.part_o + row * D + c4 * 4) = acc;
-                        if (c4 == 0) p.part_ml[row] = make_float2(m, l);
+                        *reinterpret_cast<float4*>(p.parts.o + row * D + c4 * 4) = acc;
+                        if (c4 == 0) p.parts.ml[row] = make_float2(m, l);
                     } else {
                         const float inv = l > 0.f ? 1.0f / l : 0.f;
                         const int row = t.row0 + r / p.G, h = t.head * p.G + r % p.G;
@@ -392,7 +393,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 }
 
 template <int D>
-int launch_decode_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cudaStream_t stream) {
+int launch_decode_d(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream) {
     using C = DecodeCfg<D>;
     const int rows = std::min(a.cache.page_size, C::KT);
     CUtensorMap mk, mv;
@@ -400,29 +401,22 @@ int launch_decode_d(const PagedAttnArgs& a, PagedParams p, void* workspace, cuda
         return ULYSSES_ERR_CUDA;
     auto kern = paged_decode_kernel<D>;
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ULYSSES_ERR_CUDA;
-    const int ctas = std::min(2 * device_sm_count(), kDecodeMaxCtas);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.part_o = reinterpret_cast<float*>(ws);
-    ws += size_t(2) * kDecodeMaxCtas * kDecodeRows * D * 4;
-    p.part_ml = reinterpret_cast<float2*>(ws);
-    ws += size_t(2) * kDecodeMaxCtas * kDecodeRows * 8;
-    p.meta = reinterpret_cast<PagedMeta*>(ws);
-    kern<<<ctas, kDecodeThreads, C::SMEM_BYTES, stream>>>(mk, mv, p, __builtin_ctz(unsigned(rows)));
-    if (cudaGetLastError() != cudaSuccess) return ULYSSES_ERR_CUDA;
-    return launch_paged_join<D, kDecodeRows>(p, ctas, stream);
+    if (!launch_chained(kern, dim3(unsigned(p.parts.ctas)), kDecodeThreads, C::SMEM_BYTES, stream, mk, mv, p,
+                        __builtin_ctz(unsigned(rows))))
+        return ULYSSES_ERR_CUDA;
+    return ULYSSES_OK;
 }
 
 }  // namespace
 
 int paged_decode_rows() { return kDecodeRows; }
 
-size_t paged_decode_workspace_bytes(int d_h) {
-    const size_t n = size_t(2) * kDecodeMaxCtas * kDecodeRows * (size_t(d_h) * 4 + 8) + kDecodeMaxCtas * sizeof(PagedMeta);
-    return (n + 255) / 256 * 256;
+PagedParts paged_decode_parts(void* workspace, int d_h, size_t* bytes) {
+    return paged_parts(workspace, kDecodeMaxCtas, std::min(2 * device_sm_count(), kDecodeMaxCtas), kDecodeRows, d_h, bytes);
 }
 
-int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, void* workspace, cudaStream_t stream) {
-    return a.cache.d_h == 128 ? launch_decode_d<128>(a, p, workspace, stream) : launch_decode_d<64>(a, p, workspace, stream);
+int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream) {
+    return a.cache.d_h == 128 ? launch_decode_d<128>(a, p, stream) : launch_decode_d<64>(a, p, stream);
 }
 
 }  // namespace ulysses

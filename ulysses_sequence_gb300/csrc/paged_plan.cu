@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     int32_t* pg = cu + p.B + 1;          // [B + 1] new pages before each request
     int32_t* held = pg + p.B + 1;        // [B] cached tokens, clamped
     __shared__ uint32_t warp_sums[kPlanThreads / 32];
+    grid_wait();
+    grid_release();
     const int page = 1 << p.page_shift;
     const int cap = p.max_pages << p.page_shift;
     const int n_free = min(max(*p.n_free, 0), p.free_capacity);
@@ -204,25 +206,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     const uint32_t r0 = uint32_t(base - t0 * p.row) + threadIdx.x;
     const int w = blockIdx.y;
     uint4 v[kAppendUnroll];
-    uint4* to[kAppendUnroll];
+    uint32_t c[kAppendUnroll];
+    int slot[kAppendUnroll];
+    grid_wait();
+    grid_release();
+    // rows and slots together: a skipped token's row is read all the same
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u) {
-        to[u] = nullptr;
+        slot[u] = -1;
+        const uint32_t r = r0 + u * kAppendThreads, dt = r / uint32_t(p.row);
+        c[u] = r - dt * p.row;
         if (base + threadIdx.x + u * kAppendThreads < p.pieces) {
-            const uint32_t r = r0 + u * kAppendThreads, dt = r / uint32_t(p.row), c = r - dt * p.row;
-            const int64_t t = t0 + dt;
-            const int slot = p.slots[t];
-            if (unsigned(slot) < unsigned(p.n_slots)) {
-                const uint32_t h = c / uint32_t(p.head), e = c - h * p.head;
-                const int page = slot >> p.page_shift, token = slot & ((1 << p.page_shift) - 1);
-                v[u] = p.src[w][t * p.src_stride[w] + c];
-                to[u] = p.dst[w] + page * p.page_stride + token * p.token_stride + h * p.head_stride + e;
-            }
+            slot[u] = p.slots[t0 + dt];
+            v[u] = p.src[w][(t0 + dt) * p.src_stride[w] + c[u]];
         }
     }
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u)
-        if (to[u]) *to[u] = v[u];
+    for (int u = 0; u < kAppendUnroll; ++u) {
+        if (unsigned(slot[u]) < unsigned(p.n_slots)) {
+            const uint32_t h = c[u] / uint32_t(p.head), e = c[u] - h * p.head;
+            const int page = slot[u] >> p.page_shift, token = slot[u] & ((1 << p.page_shift) - 1);
+            p.dst[w][page * p.page_stride + token * p.token_stride + h * p.head_stride + e] = v[u];
+        }
+    }
 }
 
 }  // namespace
@@ -238,8 +244,7 @@ int launch_page_plan(int B, int T, int page_shift, int max_pages, int64_t table_
         return ULYSSES_ERR_CUDA;
     const int64_t want = (int64_t(T) + kPlanThreads - 1) / kPlanThreads;
     const int grid = int(std::max<int64_t>(1, std::min<int64_t>(want, device_sm_count())));
-    page_plan_kernel<<<grid, kPlanThreads, smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
+    return launch_chained(page_plan_kernel, dim3(unsigned(grid)), kPlanThreads, size_t(smem), stream, p) ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 
 int launch_kv_append(const ulysses_kv_cache_t& c, int T, const void* k, int64_t k_stride, const void* v,
@@ -262,8 +267,7 @@ int launch_kv_append(const ulysses_kv_cache_t& c, int T, const void* k, int64_t 
     p.n_slots = c.num_pages * c.page_size;
     const int64_t per = kAppendThreads * kAppendUnroll, blocks = (p.pieces + per - 1) / per;
     if (blocks > 0x7fffffffll) return ULYSSES_ERR_UNSUPPORTED;
-    kv_append_kernel<<<dim3(unsigned(blocks), 2), kAppendThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? ULYSSES_OK : ULYSSES_ERR_CUDA;
+    return launch_chained(kv_append_kernel, dim3(unsigned(blocks), 2), kAppendThreads, 0, stream, p) ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 
 }  // namespace ulysses
