@@ -508,12 +508,13 @@ def _call_stream(x, stream, where: str) -> int:
     """The CUDA stream of one call on x's device, which must be the current one: the caller's, or the
     current stream."""
     import torch
-    if not x.is_cuda:
+    device = x.get_device()
+    if device < 0:
         raise ValueError(f"{where}: tensors must be on a CUDA device")
-    if x.get_device() != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{where}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)  # current_stream().cuda_stream without the objects
     if stream.device != x.device:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {x.device}")
     return stream.cuda_stream
@@ -528,35 +529,35 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _check_tensor(x, shape, dtype, device, name: str, where: str) -> None:
-    """x is contiguous, of this shape and type, on this device."""
-    if x.shape == shape and x.dtype is dtype and x.device == device and x.is_contiguous():
+def _check_tensor(x, shape, dtype, device: int, name: str, where: str) -> None:
+    """x is contiguous, of this shape and type, on the device of this index."""
+    if x.shape == shape and x.dtype is dtype and x.get_device() == device and x.is_contiguous():
         return
-    raise ValueError(f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on {device}, got {x.dtype} "
+    raise ValueError(f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on device {device}, got {x.dtype} "
                      f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
-def _check_table(x, B: int, device, where: str) -> int:
+def _check_table(x, B: int, device: int, where: str) -> int:
     """Row stride of an int32 block table [B][max_pages] with contiguous rows on this device."""
     import torch
-    if (x.dtype is torch.int32 and x.dim() == 2 and x.shape[0] == B and x.device == device
+    if (x.dtype is torch.int32 and x.dim() == 2 and x.shape[0] == B and x.get_device() == device
             and (x.shape[1] < 2 or B == 0 or x.stride(1) == 1)):
         return x.stride(0) if B > 1 else x.shape[1]
-    raise ValueError(f"{where}: block_table must be int32 [{B}][max_pages] with contiguous rows on {device}, got "
-                     f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+    raise ValueError(f"{where}: block_table must be int32 [{B}][max_pages] with contiguous rows on device {device}, "
+                     f"got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
-def _check_rows(x, T: int, heads: int, d: int, device, name: str, where: str) -> int:
+def _check_rows(x, T: int, heads: int, d: int, device: int, name: str, where: str) -> int:
     """Row stride of bf16 token rows [T][heads][d] whose rows are contiguous, on this device."""
     import torch
-    if x.shape == (T, heads, d) and x.dtype is torch.bfloat16 and x.device == device:
+    if x.shape == (T, heads, d) and x.dtype is torch.bfloat16 and x.get_device() == device:
         if T == 0:
             return heads * d
         row, head, one = x.stride()
         if one == 1 and (heads == 1 or head == d):
             return row if T > 1 else heads * d
-    raise ValueError(f"{where}: {name} must be bf16 [{T}][{heads}][{d}] with contiguous rows on {device}, got {x.dtype} "
-                     f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
+    raise ValueError(f"{where}: {name} must be bf16 [{T}][{heads}][{d}] with contiguous rows on device {device}, got "
+                     f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
 class PagedCache:
@@ -571,7 +572,7 @@ class PagedCache:
             raise ValueError("PagedCache: k and v must be bf16 with contiguous heads")
         if not k.is_cuda or k.device != v.device:
             raise ValueError("PagedCache: k and v must be on one CUDA device")
-        self.k, self.v, self.device = k, v, k.device
+        self.k, self.v, self.device = k, v, k.get_device()
         self.num_pages, self.page_size, self.H_kv, self.d = k.shape
         self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, k.stride(0), k.stride(1), k.stride(2))
 
@@ -591,7 +592,7 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     info [4] = rows planned, pages taken, pages missing, tokens dropped). The list is not changed:
     ``n_free -= info[1:2]`` keeps the pages."""
     import torch
-    where, B, dev, i32 = "page_plan", block_table.shape[0], block_table.device, torch.int32
+    where, B, dev, i32 = "page_plan", block_table.shape[0], block_table.get_device(), torch.int32
     table_stride = _check_table(block_table, B, dev, where)
     _check_tensor(cached_lens, (B,), i32, dev, "cached_lens", where)
     _check_tensor(new_lens, (B,), i32, dev, "new_lens", where)
@@ -606,10 +607,10 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
             _check_tensor(x, (n,), i32, dev, name, where)
         outs.append(x)
     cu_q, kv_lens, slot_map, info = outs
-    check(ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
-                            new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                            block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
-                            info.data_ptr(), st), where)
+    check(load().ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
+                                   new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                                   block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
+                                   info.data_ptr(), st), where)
     return cu_q, kv_lens, slot_map, info
 
 
@@ -621,8 +622,8 @@ def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
     k_stride = _check_rows(k, T, cache.H_kv, cache.d, dev, "k", where)
     v_stride = _check_rows(v, T, cache.H_kv, cache.d, dev, "v", where)
     _check_tensor(slot_map, (T,), torch.int32, dev, "slot_map", where)
-    check(ulysses_kv_append(cache.struct, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
-                            _call_stream(cache.k, stream, where)), where)
+    check(load().ulysses_kv_append(ctypes.byref(cache.struct), T, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                   slot_map.data_ptr(), _call_stream(cache.k, stream, where)), where)
 
 
 def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
@@ -662,12 +663,13 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
     if workspace is None:
         n = ulysses_paged_attn_workspace_size(H, cache.H_kv, d, max_q)
         workspace = _new((max(n, 256),), torch.uint8, q, stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"{where}: workspace must be contiguous on {dev}")
-    check(ulysses_paged_attn_fwd(cache.struct, B, T, H, max_q, MASK_CAUSAL if mask is None else mask.kind, window, scale,
-                                 q.data_ptr(), q_stride, cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
-                                 table_stride, block_table.shape[1], o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), st), where)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous on device {dev}")
+    check(load().ulysses_paged_attn_fwd(ctypes.byref(cache.struct), B, T, H, max_q,
+                                        MASK_CAUSAL if mask is None else mask.kind, window, scale, q.data_ptr(), q_stride,
+                                        cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), table_stride,
+                                        block_table.shape[1], o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), st), where)
     return o, lse
 
 
