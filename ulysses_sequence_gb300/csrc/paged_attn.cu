@@ -63,6 +63,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.min_rows = 1;
     if (decode_fits(p.G)) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
+        p.unit_tokens = paged_decode_rows() / p.G;
         p.parts = decode = paged_decode_parts(ws, d, &bytes);
         const int rc = launch_paged_decode(a, p, stream);
         if (rc != ULYSSES_OK) return rc;
@@ -70,6 +71,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     }
     if (!only) {
         p.max_rows = 0x7fffffff;
+        p.unit_tokens = 2 * (kTile / p.G);
         p.parts = chunk = paged_chunk_parts(ws + bytes, d, &bytes);
         const int rc = launch_paged_chunk(a, p, decode_fits(p.G), stream);
         if (rc != ULYSSES_OK) return rc;

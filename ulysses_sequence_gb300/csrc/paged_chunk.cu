@@ -121,18 +121,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         *abort_flag = 0;
         fence_mbar_init();
     }
-    const int TOK = kTile / p.G, TQ = 2 * TOK;  // tokens of a tile, of a unit
+    const int TOK = p.unit_tokens / 2;  // tokens of a tile
     if (!behind_decode) grid_wait();
-    PagedWalk<kTile, kChunkUnitCost> w;
     const int cta = int(blockIdx.x);
-    const bool work = paged_share<kTile, kChunkUnitCost, kChunkThreads>(p, TQ, kChunkMinCost,
-                                                                        reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
-    __syncthreads();
-    if (!work) {
-        if (threadIdx.x == 0) p.parts.meta[cta] = PagedMeta{0, 0, 0, 0};
-        if (behind_decode) grid_wait();
-        return;
-    }
+    PagedWalk<kTile, kChunkUnitCost> w;
+    int64_t* costs = reinterpret_cast<int64_t*>(smem);  // before the first copy
+    if (p.B <= kFewRequests) paged_costs<kTile, kChunkUnitCost, kChunkThreads>(p, costs);
+    else paged_share_block<kTile, kChunkUnitCost, kChunkThreads>(p, kChunkMinCost, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -147,6 +142,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
+        if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
         // a copy is one page (or 128 keys of a longer one) by 64 elements, or by the whole head where one
         // copy fills the tile; lane l copies page l / per, 64-element chunk l % per
         const int per = log_rows == 7 ? 1 : D / 64;
@@ -168,7 +164,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int off, tiles;
             w.take(off, tiles);
             if (tiles == 0) {
-                if (w.left > 0) w.next_unit(p, TQ);
+                if (w.left > 0) w.next_unit(p);
                 continue;
             }
             const int tokens = w.t1 - w.t0, row0 = w.s.start + w.t0, pos = w.s.base + w.t0;
@@ -232,7 +228,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (!ok) break;
             ++piece;
-            if (w.left > 0) w.next_unit(p, TQ);
+            if (w.left > 0) w.next_unit(p);
         }
         if (ok && (piece < 2 || (ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 5))) && lane == 0) {
             pieces[piece & 1].tiles = 0;
@@ -495,7 +491,7 @@ int launch_chunk_d(const PagedAttnArgs& a, const PagedParams& p, bool behind_dec
     const int chunks = rows == kTile ? D / 64 : 1;
     CUtensorMap mq, mk, mv;
     {
-        const int tok = kTile / p.G;
+        const int tok = p.unit_tokens / 2;
         cuuint64_t dims[5] = {64, cuuint64_t(p.H), cuuint64_t(p.T), D / 64, 1};
         cuuint64_t strides[4] = {D * 2, cuuint64_t(p.q_stride) * 2, 128, 128};
         cuuint32_t box[5] = {64, cuuint32_t(p.G), cuuint32_t(tok), 1, 1};

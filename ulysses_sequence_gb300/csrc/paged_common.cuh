@@ -38,6 +38,7 @@ struct PagedParams {
     int causal, window;
     int min_rows;            // requests with fewer rows (new tokens x G) than this are left to the other kernel
     int max_rows;            // and those with more
+    int unit_tokens;         // new tokens of a unit
     float scale_log2;
     int64_t q_stride, table_stride;
     const __nv_bfloat16* q;
@@ -86,8 +87,10 @@ __device__ __forceinline__ void paged_tiles(const PagedParams& p, const PagedSeq
 
 // Cost of one head of a request, over its row tiles of TQ tokens; OVH is a unit's fixed part.
 template <int KT, int OVH>
-__device__ __forceinline__ int64_t paged_head_cost(const PagedParams& p, const PagedSeq& s, int TQ) {
+__device__ __forceinline__ int64_t paged_head_cost(const PagedParams& p, const PagedSeq& s) {
+    const int TQ = p.unit_tokens;
     int64_t sum = 0;
+#pragma unroll 1
     for (int t0 = 0; t0 < s.n; t0 += TQ) {
         int first, count;
         paged_tiles<KT>(p, s, t0, min(s.n, t0 + TQ), first, count);
@@ -107,8 +110,8 @@ struct PagedWalk {
     int64_t W;               // the line's cost
     int n;                   // CTAs with work (the first ones)
 
-    __device__ __forceinline__ void unit(const PagedParams& p, int TQ) {
-        t1 = min(s.n, t0 + TQ);
+    __device__ __forceinline__ void unit(const PagedParams& p) {
+        t1 = min(s.n, t0 + p.unit_tokens);
         paged_tiles<KT>(p, s, t0, t1, first, count);
     }
     // This CTA's part of the unit, key tiles [off, off + tiles), possibly none.
@@ -143,9 +146,9 @@ struct PagedWalk {
         }
         s.n = 0;
     }
-    __device__ __forceinline__ void next_unit(const PagedParams& p, int TQ) {
+    __device__ __forceinline__ void next_unit(const PagedParams& p) {
         pos = 0;
-        t0 += TQ;
+        t0 += p.unit_tokens;
         if (t0 >= s.n) {
             t0 = 0;
             if (++head == p.Hkv) {
@@ -153,7 +156,7 @@ struct PagedWalk {
                 next_request(p);
             }
         }
-        unit(p, TQ);
+        unit(p);
     }
 };
 
@@ -180,31 +183,14 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* sh, int64_t&
     return v + before;
 }
 
-// Where this CTA's share of the line begins. All threads of the block call it (NT threads, a whole
-// number of warps); every warp leaves with the same walk. False for a CTA without work.
-template <int KT, int OVH, int NT>
-__device__ __forceinline__ bool paged_share(const PagedParams& p, int TQ, int min_cost, int64_t* sh /* [NT / 32 + 2] */,
-                                            PagedWalk<KT, OVH>& w) {
-    constexpr int NW = NT / 32;
-    constexpr int KEEP = 4;  // requests whose cost a thread keeps from the first pass
-    const int tid = int(threadIdx.x), lane = tid & 31;
-    auto cost_of = [&](int i) {
-        if (i >= p.B) return int64_t(0);
-        const PagedSeq s = paged_seq(p, i);
-        return s.n > 0 ? paged_head_cost<KT, OVH>(p, s, TQ) * p.Hkv : int64_t(0);
-    };
-    int64_t kept[KEEP], mine = 0;
-#pragma unroll
-    for (int k = 0; k < KEEP; ++k) {
-        kept[k] = k * NT < p.B ? cost_of(k * NT + tid) : 0;
-        mine += kept[k];
-    }
-    for (int i = KEEP * NT + tid; i < p.B; i += NT) mine += cost_of(i);
-    int64_t incl = block_prefix<NT>(mine, sh, w.W);
+// The CTA's end of the line, once its cost is known: false for a CTA without work.
+template <int KT, int OVH>
+__device__ __forceinline__ bool paged_cut(PagedWalk<KT, OVH>& w, int min_cost, int64_t& begin) {
     w.n = int(min(int64_t(gridDim.x), (w.W + min_cost - 1) / min_cost));
     const int c = int(blockIdx.x);
+    w.left = 0;
     if (c >= w.n) return false;
-    int64_t begin, end;
+    int64_t end;
     if (w.W < (int64_t(1) << 31)) {  // 32-bit divisions where they do
         const uint32_t W = uint32_t(w.W), n = uint32_t(w.n), q = W / n, r = W - q * n;
         begin = q * uint32_t(c) + r * uint32_t(c) / n;
@@ -214,33 +200,23 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, int TQ, int mi
         end = w.W * (c + 1) / w.n;
     }
     w.left = end - begin;
-    // the request that holds `begin`: a running prefix, NT requests at a time
-    int64_t run = 0;
-    for (int k = 0; k * NT < p.B; ++k) {
-        int64_t cost = mine, total = w.W;
-        if (p.B > NT) {
-            cost = 0;
-            if (k < KEEP) {
-#pragma unroll
-                for (int y = 0; y < KEEP; ++y)
-                    if (y == k) cost = kept[y];
-            } else {
-                cost = cost_of(k * NT + tid);
-            }
-            incl = run + block_prefix<NT>(cost, sh, total);
-        }
-        if (begin >= incl - cost && begin < incl) {
-            sh[NW] = k * NT + tid;
-            sh[NW + 1] = begin - (incl - cost);
-        }
-        run += total;
-        if (begin < run) break;  // the same in all threads
+    return true;
+}
+
+// The walk's first unit, `rem` into request i: the head, then the row tile, 32 looked at at a time.
+template <int KT, int OVH>
+__device__ __forceinline__ void paged_start(const PagedParams& p, int i, int64_t rem, PagedWalk<KT, OVH>& w) {
+    const int lane = int(lane_id()), TQ = p.unit_tokens;
+    w.i = i;
+    w.s = paged_seq(p, i);
+    w.t0 = 0;
+    if (w.s.n <= TQ) {
+        w.unit(p);
+        const int cost = OVH + w.count;
+        w.head = w.W < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(cost)) : int(rem / cost);
+        w.pos = int(rem - int64_t(cost) * w.head);
+        return;
     }
-    __syncthreads();
-    w.i = int(sh[NW]);
-    int64_t rem = sh[NW + 1];
-    w.s = paged_seq(p, w.i);
-    // the head, then the row tile, 32 looked at at a time
     int64_t per_head = 0;
     for (int64_t t = int64_t(lane) * TQ; t < w.s.n; t += int64_t(32) * TQ) {
         int first, count;
@@ -249,33 +225,101 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, int TQ, int mi
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, o);
-    w.head = w.W < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(per_head)) : int(rem / per_head);
+    w.head = int(rem / per_head);
     rem -= per_head * w.head;
-    w.t0 = 0;
-    w.pos = int(rem);
-    if (w.s.n > TQ) {
-        for (int64_t a = 0; a < w.s.n; a += int64_t(32) * TQ) {
-            const int64_t t = a + int64_t(lane) * TQ;
-            int first = 0, count = -OVH;
-            if (t < w.s.n) paged_tiles<KT>(p, w.s, int(t), int(min(int64_t(w.s.n), t + TQ)), first, count);
-            const int64_t cost = count + OVH;
-            int64_t sum = cost;
+    for (int64_t a = 0; a < w.s.n; a += int64_t(32) * TQ) {
+        const int64_t t = a + int64_t(lane) * TQ;
+        int first = 0, count = -OVH;
+        if (t < w.s.n) paged_tiles<KT>(p, w.s, int(t), int(min(int64_t(w.s.n), t + TQ)), first, count);
+        const int64_t cost = count + OVH;
+        int64_t sum = cost;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += y;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, rem >= sum - cost && rem < sum);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                w.t0 = int(a) + src * TQ;
-                w.pos = int(rem - __shfl_sync(0xffffffffu, sum - cost, src));
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, sum, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
         }
+        const unsigned hit = __ballot_sync(0xffffffffu, rem >= sum - cost && rem < sum);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            w.t0 = int(a) + src * TQ;
+            w.pos = int(rem - __shfl_sync(0xffffffffu, sum - cost, src));
+            break;
+        }
+        rem -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    w.unit(p, TQ);
+    w.unit(p);
+}
+
+template <int KT, int OVH>
+__device__ __forceinline__ int64_t paged_cost(const PagedParams& p, int i) {
+    if (i >= p.B) return 0;
+    const PagedSeq s = paged_seq(p, i);
+    return s.n > 0 ? paged_head_cost<KT, OVH>(p, s) * p.Hkv : int64_t(0);
+}
+
+// Where this CTA's share of the line begins, for batches of up to kFewRequests requests, in two steps with
+// the block's barrier between them: every thread puts down a request's cost, then one warp finds the
+// place. The code runs once a launch, so it is kept short: its instruction fetches are most of its time.
+constexpr int kFewRequests = 256;
+template <int KT, int OVH, int NT>
+__device__ __forceinline__ void paged_costs(const PagedParams& p, int64_t* costs /* [kFewRequests] */) {
+#pragma unroll 1
+    for (int i = int(threadIdx.x); i < kFewRequests; i += NT) costs[i] = paged_cost<KT, OVH>(p, i);
+    fence_proxy_async_smem();  // copies may land there next
+}
+template <int KT, int OVH>
+__device__ __forceinline__ bool paged_share_warp(const PagedParams& p, int min_cost, const int64_t* costs, PagedWalk<KT, OVH>& w) {
+    const int lane = int(lane_id()), per = (p.B + 31) / 32;  // consecutive requests of a lane
+    int64_t mine = 0;
+#pragma unroll 1
+    for (int k = 0; k < per; ++k) mine += costs[lane * per + k];
+    int64_t incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    w.W = __shfl_sync(0xffffffffu, incl, 31);
+    int64_t begin;
+    if (!paged_cut(w, min_cost, begin)) return false;
+    int64_t rem = begin - (incl - mine);
+    const int src = __ffs(__ballot_sync(0xffffffffu, rem >= 0 && rem < mine)) - 1;
+    int i = __shfl_sync(0xffffffffu, lane * per, src);
+    rem = __shfl_sync(0xffffffffu, rem, src);
+#pragma unroll 1
+    while (rem >= costs[i]) rem -= costs[i++];
+    fence_proxy_async_smem();
+    paged_start(p, i, rem, w);
+    return true;
+}
+
+// The same for any batch: all threads of the block call it (NT threads, a whole number of warps), and
+// every warp leaves with the same walk.
+template <int KT, int OVH, int NT>
+__device__ __forceinline__ bool paged_share_block(const PagedParams& p, int min_cost, int64_t* sh /* [NT / 32 + 2] */,
+                                                  PagedWalk<KT, OVH>& w) {
+    constexpr int NW = NT / 32;
+    const int tid = int(threadIdx.x);
+    int64_t mine = 0;
+    for (int i = tid; i < p.B; i += NT) mine += paged_cost<KT, OVH>(p, i);
+    block_prefix<NT>(mine, sh, w.W);
+    int64_t begin;
+    if (!paged_cut(w, min_cost, begin)) return false;
+    // the request that holds `begin`: a running prefix, NT requests at a time
+    int64_t run = 0;
+    for (int a = 0; a < p.B; a += NT) {
+        const int64_t cost = paged_cost<KT, OVH>(p, a + tid);
+        int64_t total;
+        const int64_t incl = run + block_prefix<NT>(cost, sh, total);
+        if (begin >= incl - cost && begin < incl) {
+            sh[NW] = a + tid;
+            sh[NW + 1] = begin - (incl - cost);
+        }
+        run += total;
+        if (begin < run) break;  // the same in all threads
+    }
+    __syncthreads();
+    paged_start(p, int(sh[NW]), sh[NW + 1], w);
     return true;
 }
 

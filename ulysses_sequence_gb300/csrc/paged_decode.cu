@@ -105,18 +105,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         *abort_flag = 0;
         fence_mbar_init();
     }
-    const int TQ = kDecodeRows / p.G;
     grid_wait();
     grid_release();  // not before the wait: the chunk kernel starts behind this without one
-    PagedWalk<C::KT, kDecodeUnitCost> w;
     const int cta = int(blockIdx.x);
-    const bool work = paged_share<C::KT, kDecodeUnitCost, kDecodeThreads>(p, TQ, kDecodeMinCost,
-                                                                          reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    PagedWalk<C::KT, kDecodeUnitCost> w;
+    int64_t* costs = reinterpret_cast<int64_t*>(smem);  // before the first copy
+    if (p.B <= kFewRequests) paged_costs<C::KT, kDecodeUnitCost, kDecodeThreads>(p, costs);
+    else paged_share_block<C::KT, kDecodeUnitCost, kDecodeThreads>(p, kDecodeMinCost, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     __syncthreads();
-    if (!work) {
-        if (threadIdx.x == 0) p.parts.meta[cta] = PagedMeta{0, 0, 0, 0};
-        return;
-    }
     const Abort ab{abort_flag, p.err, KID_PAGED};
 
     if (warp == 0) {
@@ -125,11 +121,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
+        if (p.B <= kFewRequests) paged_share_warp(p, kDecodeMinCost, costs, w);
         const int copies = 2 * (C::KT >> log_rows);  // one per page and operand
         const int my_row = (lane >> 1) << log_rows;  // of this lane's copy within the tile
-        auto lookup = [&](int key0) {
+        int lo, hi;                                  // keys that the unit's rows may see
+        auto lookup = [&](int key0) {                // only their pages are copied
             const int key = key0 + my_row;
-            return lane < copies && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
+            return lane < copies && key < hi && key + (1 << log_rows) > lo ? p.table[w.i * p.table_stride + (key >> p.page_shift)]
+                                                                           : -1;
         };
         PagedMeta meta{0, 0, 0, 0};
         int issued = 0;
@@ -153,6 +152,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
                 first_piece = false;
                 const int rows = (w.t1 - w.t0) * p.G;
+                paged_range(p, w.s, w.t0, w.t1, lo, hi);
                 int id = lookup((w.first + off) * C::KT);
                 for (int x = 0; x < tiles; ++x) {
                     const int st = issued % C::STAGES;
@@ -160,8 +160,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const int id_next = x + 1 < tiles ? lookup(key0 + C::KT) : -1;
                     if (!free_stage(st)) break;
                     const bool good = unsigned(id) < unsigned(p.num_pages);
-                    // one bit per copy (the K copy of each page), spread to 16 keys a bit
-                    const unsigned pages = __ballot_sync(0xffffffffu, good && (lane & 1) == 0);
+                    // one bit per copy, and one per 16 keys
+                    const unsigned pages = __ballot_sync(0xffffffffu, good);
                     const int page_of = (min(lane, C::KT / 16 - 1) * 16) >> log_rows;  // of keys [16 lane, 16 lane + 16)
                     const uint32_t valid = __ballot_sync(0xffffffffu, lane < C::KT / 16 && ((pages >> (2 * page_of)) & 1u));
                     uint8_t* stage = smem + st * C::STAGE_BYTES;
@@ -175,15 +175,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         t.rows = rows; t.row0 = w.s.start + w.t0; t.head = w.head; t.slot = slot;
                         t.valid = valid;
                         *tile_desc(st) = t;
-                        mbar_arrive_expect_tx(full + st, C::STAGE_BYTES + (x == 0 ? rows * D * 2 : 0));
+                        mbar_arrive_expect_tx(full + st, (__popc(pages) << log_rows) * (D * 2) + (x == 0 ? rows * D * 2 : 0));
                     }
                     __syncwarp();
-                    if (lane < copies) {
-                        // a page that does not exist is copied from behind the pool: zeros
-                        const int page = good ? id : p.num_pages, row = (key0 + my_row) & ((1 << p.page_shift) - 1);
+                    if (good)
                         tma_load_5d(stage + (lane & 1) * C::KV_BYTES + my_row * (D * 2), (lane & 1) ? &tm_v : &tm_k, full + st, 0,
-                                    row, w.head, page, 0);
-                    }
+                                    (key0 + my_row) & ((1 << p.page_shift) - 1), w.head, id, 0);
                     if (x == 0 && lane < rows) {
                         const __nv_bfloat16* src = p.q + int64_t(w.s.start + w.t0 + lane / p.G) * p.q_stride +
                                                    int64_t(w.head * p.G + lane % p.G) * D;
@@ -193,7 +190,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     id = id_next;
                 }
             }
-            if (ok && w.left > 0) w.next_unit(p, TQ);
+            if (ok && w.left > 0) w.next_unit(p);
         }
         if (lane == 0) p.parts.meta[cta] = meta;
         if (ok && free_stage(issued % C::STAGES)) {
@@ -308,12 +305,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int j = 0; j < NT / 2; ++j) {
                 const uint32_t a[4] = {pack_bf16(s[2 * j][0], s[2 * j][1]), pack_bf16(s[2 * j][2], s[2 * j][3]),
                                        pack_bf16(s[2 * j + 1][0], s[2 * j + 1][1]), pack_bf16(s[2 * j + 1][2], s[2 * j + 1][3])};
-                // values behind the last key may be anything, NaN too: their bits are cleared
+                // values behind the last key, or of pages that were not copied, may be anything, NaN too:
+                // their bits are cleared
                 uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
                 if (masked) {
-                    const int key = col + j * 16;
-                    keep0 = (key < t.kv ? 0xffffu : 0u) | (key + 1 < t.kv ? 0xffff0000u : 0u);
-                    keep1 = (key + 8 < t.kv ? 0xffffu : 0u) | (key + 9 < t.kv ? 0xffff0000u : 0u);
+                    const int end = (t.valid >> ((cw * C::KW + j * 16) >> 4)) & 1u ? t.kv : 0, key = col + j * 16;
+                    keep0 = (key < end ? 0xffffu : 0u) | (key + 1 < end ? 0xffff0000u : 0u);
+                    keep1 = (key + 8 < end ? 0xffffu : 0u) | (key + 9 < end ? 0xffff0000u : 0u);
                 }
                 const int key = cw * C::KW + j * 16 + (lane & 15);
 #pragma unroll
