@@ -182,11 +182,26 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
 }
 
 // ---------------------------------------------------------------------------------------
-// kv_append: a gather of rows by slot with nothing to compute, bound by its reads and writes
-// (one each of 4 H_kv d_h bytes a token). A CTA moves 16-byte pieces of consecutive tokens, four per
-// thread, all four loads in flight before the first store; grid row 0 moves keys, row 1 values.
+// kv_append: rows moved by slot with nothing to compute, bound by its reads and writes (one each of
+// 4 H_kv d_h bytes a token). A CTA moves 16-byte pieces of consecutive tokens, U per thread, all of a
+// thread's loads in flight before its first store; grid row 0 moves keys, row 1 values. Many pieces per
+// thread pay when there are many (starting a CTA costs more than its few copies: 32768 tokens of 8 heads
+// of 128 take 41.6 us with 16 pieces, 6.45 TB/s, and 76 us with two), few when there are few (128 tokens:
+// 1.5 us with two, 2.8 us with 16); the two meet near 768 tokens.
 // ---------------------------------------------------------------------------------------
-constexpr int kAppendThreads = 256, kAppendUnroll = 4;
+constexpr int kAppendThreads = 128, kAppendFew = 2, kAppendMany = 16;
+constexpr int64_t kAppendManyPieces = 48 * kAppendThreads * kAppendMany;  // from here on, by key rows' pieces
+
+// n / d for n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and m = floor(2^32 (2^s - d) / d) + 1, the
+// quotient is floor((floor(n m / 2^32) + n) / 2^s).
+struct FastDiv {
+    uint32_t d, m, s;
+    explicit FastDiv(uint32_t div = 1) : d(div), m(0), s(0) {
+        while ((uint64_t(1) << s) < d) ++s;
+        m = uint32_t((((uint64_t(1) << s) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
 
 struct AppendParams {
     const uint4* src[2];
@@ -195,38 +210,42 @@ struct AppendParams {
     int64_t page_stride, token_stride, head_stride;  // 16-byte pieces
     const int32_t* slots;
     int64_t pieces;                 // T * row pieces
-    int row, head;                  // pieces of a token, of a head
+    FastDiv row, head;              // pieces of a token, of a head
     int page_shift;
     int n_slots;                    // num_pages * page_size
 };
 
+template <int U>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
-    const int64_t base = int64_t(blockIdx.x) * (kAppendThreads * kAppendUnroll);
-    const int64_t t0 = base / p.row;
-    const uint32_t r0 = uint32_t(base - t0 * p.row) + threadIdx.x;
-    const int w = blockIdx.y;
-    uint4 v[kAppendUnroll];
-    uint32_t c[kAppendUnroll];
-    int slot[kAppendUnroll];
+    const int64_t base = int64_t(blockIdx.x) * (kAppendThreads * U);
+    const int64_t t0 = p.pieces < (int64_t(1) << 31) ? int64_t(p.row(uint32_t(base))) : base / p.row.d;
+    const uint32_t r0 = uint32_t(base - t0 * p.row.d) + threadIdx.x;
+    const bool key = blockIdx.y == 0;
+    const uint4* src = key ? p.src[0] : p.src[1];
+    uint4* dst = key ? p.dst[0] : p.dst[1];
+    const int64_t src_stride = key ? p.src_stride[0] : p.src_stride[1];
+    uint4 v[U];
+    uint32_t c[U];
+    int slot[U];
     grid_wait();
     grid_release();
     // rows and slots together: a skipped token's row is read all the same
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
         slot[u] = -1;
-        const uint32_t r = r0 + u * kAppendThreads, dt = r / uint32_t(p.row);
-        c[u] = r - dt * p.row;
+        const uint32_t r = r0 + u * kAppendThreads, dt = p.row(r);
+        c[u] = r - dt * p.row.d;
         if (base + threadIdx.x + u * kAppendThreads < p.pieces) {
             slot[u] = p.slots[t0 + dt];
-            v[u] = p.src[w][(t0 + dt) * p.src_stride[w] + c[u]];
+            v[u] = src[(t0 + dt) * src_stride + c[u]];
         }
     }
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
         if (unsigned(slot[u]) < unsigned(p.n_slots)) {
-            const uint32_t h = c[u] / uint32_t(p.head), e = c[u] - h * p.head;
+            const uint32_t h = p.head(c[u]), e = c[u] - h * p.head.d;
             const int page = slot[u] >> p.page_shift, token = slot[u] & ((1 << p.page_shift) - 1);
-            p.dst[w][page * p.page_stride + token * p.token_stride + h * p.head_stride + e] = v[u];
+            dst[page * p.page_stride + token * p.token_stride + h * p.head_stride + e] = v[u];
         }
     }
 }
@@ -260,14 +279,16 @@ int launch_kv_append(const ulysses_kv_cache_t& c, int T, const void* k, int64_t 
     p.token_stride = c.token_stride / 8;
     p.head_stride = c.head_stride / 8;
     p.slots = slots;
-    p.head = c.d_h / 8;
-    p.row = c.H_kv * p.head;
-    p.pieces = int64_t(T) * p.row;
+    p.head = FastDiv(uint32_t(c.d_h / 8));
+    p.row = FastDiv(uint32_t(c.H_kv) * p.head.d);
+    p.pieces = int64_t(T) * p.row.d;
     p.page_shift = __builtin_ctz(unsigned(c.page_size));
     p.n_slots = c.num_pages * c.page_size;
-    const int64_t per = kAppendThreads * kAppendUnroll, blocks = (p.pieces + per - 1) / per;
+    const bool many = p.pieces >= kAppendManyPieces;
+    const int64_t per = kAppendThreads * (many ? kAppendMany : kAppendFew), blocks = (p.pieces + per - 1) / per;
     if (blocks > 0x7fffffffll) return ULYSSES_ERR_UNSUPPORTED;
-    return launch_chained(kv_append_kernel, dim3(unsigned(blocks), 2), kAppendThreads, 0, stream, p) ? ULYSSES_OK : ULYSSES_ERR_CUDA;
+    return launch_chained(many ? kv_append_kernel<kAppendMany> : kv_append_kernel<kAppendFew>, dim3(unsigned(blocks), 2),
+                          kAppendThreads, 0, stream, p) ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 
 }  // namespace ulysses
