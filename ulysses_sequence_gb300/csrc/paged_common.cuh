@@ -323,22 +323,21 @@ __device__ __forceinline__ bool paged_share_block(const PagedParams& p, int min_
     return true;
 }
 
-// Joins the pieces of cut units of both kernels of a call: a unit's rows are cut into blocks of 128 groups
-// of four elements, one to a thread; the blocks of the units that the CTAs of `a` opened come first, then
-// those of `b`. Bound by latency: pieces are read eight at a time, all loads of the eight in flight together.
-template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p, const PagedParts a_parts, const PagedParts b_parts) {
-    const int a_blocks = a_parts.ctas > 0 ? (a_parts.ctas - 1) * (a_parts.rows * D / 512) : 0;
+// Joins the pieces of cut units of both kernels of a call: a unit's rows are cut into blocks of NT groups of
+// four elements, one to a thread; the blocks of the units that the CTAs of `a` opened come first, then
+// those of `b`. Bound by latency: N pieces are read at a time, all their loads in flight together.
+template <int D, int NT, int N>
+__global__ void __launch_bounds__(NT) paged_join_kernel(const PagedParams p, const PagedParts a_parts, const PagedParts b_parts) {
+    const int a_blocks = a_parts.ctas > 0 ? (a_parts.ctas - 1) * (a_parts.rows * D / (4 * NT)) : 0;
     const bool second = int(blockIdx.x) >= a_blocks;
     const PagedParts& w = second ? b_parts : a_parts;
-    const int block = int(blockIdx.x) - (second ? a_blocks : 0), per = w.rows * D / 512;
+    const int block = int(blockIdx.x) - (second ? a_blocks : 0), per = w.rows * D / (4 * NT);
     const int c = block / per;
-    const int x = (block - c * per) * 128 + int(threadIdx.x), r = x / (D / 4), col = (x % (D / 4)) * 4;
+    const int x = (block - c * per) * NT + int(threadIdx.x), r = x / (D / 4), col = (x % (D / 4)) * 4;
     grid_wait();
     grid_release();
     const PagedMeta u = w.meta[c];
     if (u.pieces == 0 || r >= u.rows) return;
-    constexpr int N = 8;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int a = 0; a < u.pieces; a += N) {
