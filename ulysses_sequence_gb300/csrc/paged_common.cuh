@@ -144,7 +144,7 @@ struct PagedWalk {
                 return;
             }
         }
-        s.n = 0;
+        left = 0;  // not reached while the lengths stand still: the share ends where the requests do
     }
     __device__ __forceinline__ void next_unit(const PagedParams& p) {
         pos = 0;
@@ -213,8 +213,8 @@ __device__ __forceinline__ void paged_start(const PagedParams& p, int i, int64_t
     if (w.s.n <= TQ) {
         w.unit(p);
         const int cost = OVH + w.count;
-        w.head = w.W < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(cost)) : int(rem / cost);
-        w.pos = int(rem - int64_t(cost) * w.head);
+        w.head = min(p.Hkv - 1, w.W < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(cost)) : int(rem / cost));
+        w.pos = min(cost, int(rem - int64_t(cost) * w.head));
         return;
     }
     int64_t per_head = 0;
@@ -225,7 +225,7 @@ __device__ __forceinline__ void paged_start(const PagedParams& p, int i, int64_t
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, o);
-    w.head = int(rem / per_head);
+    w.head = int(min(int64_t(p.Hkv - 1), rem / per_head));
     rem -= per_head * w.head;
     for (int64_t a = 0; a < w.s.n; a += int64_t(32) * TQ) {
         const int64_t t = a + int64_t(lane) * TQ;
@@ -287,7 +287,7 @@ __device__ __forceinline__ bool paged_share_warp(const PagedParams& p, int min_c
     int i = __shfl_sync(0xffffffffu, lane * per, src);
     rem = __shfl_sync(0xffffffffu, rem, src);
 #pragma unroll 1
-    while (rem >= costs[i]) rem -= costs[i++];
+    while (i + 1 < p.B && rem >= costs[i]) rem -= costs[i++];
     fence_proxy_async_smem();
     paged_start(p, i, rem, w);
     return true;
@@ -306,6 +306,7 @@ __device__ __forceinline__ bool paged_share_block(const PagedParams& p, int min_
     int64_t begin;
     if (!paged_cut(w, min_cost, begin)) return false;
     // the request that holds `begin`: a running prefix, NT requests at a time
+    if (tid == 0) sh[NW] = -1;
     int64_t run = 0;
     for (int a = 0; a < p.B; a += NT) {
         const int64_t cost = paged_cost<KT, OVH>(p, a + tid);
@@ -319,6 +320,10 @@ __device__ __forceinline__ bool paged_share_block(const PagedParams& p, int min_
         if (begin < run) break;  // the same in all threads
     }
     __syncthreads();
+    if (sh[NW] < 0) {  // lengths that changed under the kernel
+        w.left = 0;
+        return false;
+    }
     paged_start(p, int(sh[NW]), sh[NW + 1], w);
     return true;
 }
