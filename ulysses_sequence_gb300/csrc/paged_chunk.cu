@@ -251,7 +251,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
+            const uint32_t one = elect_one();
+            auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_MMA, site));
+            };
             constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
             constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
             const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
@@ -261,59 +265,60 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t o = (k >> 2) * C::CHUNK_BYTES + (k & 3) * 32;
-                    umma_ss(tmem + 128 * t, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
+                    umma_ss_one(one, 128 * t, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
                 }
-                umma_commit(s_full + t);
+                umma_commit_one(one, s_full + t);
             };
             auto issue_pv = [&](int t, int sv, bool first) {  // O_t (+)= P_t V
                 const uint64_t dv = sdesc_sw128(aV + sv * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)  // 16 keys = 8 TMEM columns of P per step
-                    umma_ts(tmem + 256 + 128 * t, tmem + 128 * t + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
+                    umma_ts_one(one, 256 + 128 * t, 128 * t + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
             };
             bool ok = true;
             int j = 0, c0 = 0, c1 = 0;  // key tiles so far, PV_t so far
             for (int piece = 0; ok; ++piece) {
-                if (!(ok = mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_MMA, 1))) break;
+                if (!(ok = wait(piece_full + (piece & 1), (piece >> 1) & 1, 1))) break;
                 const int n = pieces[piece & 1].tiles;
                 const bool two = pieces[piece & 1].tokens > TOK;
                 if (n == 0) break;
-                mbar_arrive(piece_empty + (piece & 1));
-                if (!(ok = mbar_wait(q_full, piece & 1, ab, ROLE_MMA, 2))) break;
-                if (!(ok = mbar_wait(k_full + j % NSK, (j / NSK) & 1, ab, ROLE_MMA, 3))) break;
+                __syncwarp();
+                if (one) mbar_arrive(piece_empty + (piece & 1));
+                if (!(ok = wait(q_full, piece & 1, 2))) break;
+                if (!(ok = wait(k_full + j % NSK, (j / NSK) & 1, 3))) break;
                 tc_fence_after();
                 issue_s(0, j % NSK);
                 if (two) issue_s(1, j % NSK);
-                umma_commit(k_empty + j % NSK);
-                if (n == 1) umma_commit(q_empty);
+                umma_commit_one(one, k_empty + j % NSK);
+                if (n == 1) umma_commit_one(one, q_empty);
                 for (int i = 0; i < n; ++i, ++j) {
                     const bool next = i + 1 < n;
                     const int sv = j % NSV, sk = (j + 1) % NSK;
-                    if (!(ok = mbar_wait(v_full + sv, (j / NSV) & 1, ab, ROLE_MMA, 4))) break;
-                    if (!(ok = mbar_wait(p_full, c0++ & 1, ab, ROLE_MMA, 5))) break;
+                    if (!(ok = wait(v_full + sv, (j / NSV) & 1, 4))) break;
+                    if (!(ok = wait(p_full, c0++ & 1, 5))) break;
                     tc_fence_after();
                     issue_pv(0, sv, i == 0);
                     if (next) {
-                        if (!(ok = mbar_wait(k_full + sk, ((j + 1) / NSK) & 1, ab, ROLE_MMA, 6))) break;
+                        if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
                         tc_fence_after();
                         issue_s(0, sk);
                     } else {
-                        umma_commit(o_done);
+                        umma_commit_one(one, o_done);
                     }
                     if (two) {
-                        if (!(ok = mbar_wait(p_full + 1, c1++ & 1, ab, ROLE_MMA, 7))) break;
+                        if (!(ok = wait(p_full + 1, c1++ & 1, 7))) break;
                         tc_fence_after();
                         issue_pv(1, sv, i == 0);
                         if (next) issue_s(1, sk);
-                        else umma_commit(o_done + 1);
+                        else umma_commit_one(one, o_done + 1);
                     }
-                    if (next) umma_commit(k_empty + sk);
-                    if (i + 2 == n) umma_commit(q_empty);  // the piece's last scores are under way
-                    umma_commit(v_empty + sv);
+                    if (next) umma_commit_one(one, k_empty + sk);
+                    if (i + 2 == n) umma_commit_one(one, q_empty);  // the piece's last scores are under way
+                    umma_commit_one(one, v_empty + sv);
                 }
             }
             if (!ok) {
-                umma_commit(drain);
+                umma_commit_one(one, drain);
                 mbar_drain(drain, 0);
             }
         }
