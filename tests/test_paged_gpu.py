@@ -310,7 +310,149 @@ def test_offsets_past_32_bits():
     hold(o, lse, small.oracle(), 128)
 
 
+@pytest.mark.parametrize("B", [257, 700])
+@pytest.mark.parametrize("n,max_q", [(1, 1), (1, 0), (23, 23)])
+def test_many_requests(B, n, max_q):
+    """Batches beyond what one warp looks through, some requests idle."""
+    rng = np.random.default_rng(B + n)
+    reqs = [(0 if i % 9 == 4 else n, int(c)) for i, c in enumerate(rng.integers(0, 60, B))]
+    s = Step(reqs, 2, 1, 64, 16, seed=B, pad=2)
+    s.check(max_q=max_q)
+
+
+def test_keys_and_values_interleaved_in_one_allocation():
+    """Pages that hold their keys and then their values: equal strides, neither tensor contiguous."""
+    s = Step([(1, 300), (40, 77)], 8, 2, 128, 32, seed=3)
+    both = torch.empty((s.cache.num_pages, 2, 32, 2, 128), dtype=torch.bfloat16, device="cuda")
+    both[:, 0], both[:, 1] = s.k, s.v
+    s.cache = U.PagedCache(both[:, 0], both[:, 1])
+    s.check(max_q=40)
+    k, v = torch.randn(2, 5, 2, 128, device="cuda").to(torch.bfloat16)
+    before = both.clone()
+    U.kv_append(k, v, s.cache, i32([0, 33, -1, 64, 95]))
+    for t, slot in enumerate([0, 33, -1, 64, 95]):
+        if slot >= 0:
+            before[slot // 32, 0, slot % 32], before[slot // 32, 1, slot % 32] = k[t], v[t]
+    assert torch.equal(both.view(torch.int16), before.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_outputs_that_are_only_16_byte_aligned(n):
+    s = Step([(n, 100), (n, 3)], 8, 2, 64, 16, seed=n)
+    T, H, d = s.q.shape
+    o = torch.zeros(T * H * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(T, H, d)
+    lse = torch.zeros(T * H + 1, device="cuda")[1:].view(H, T)
+    assert o.data_ptr() % 32 == 16
+    U.paged_attn_fwd(s.q, s.cache, i32(s.cu), i32(s.kv), i32(s.table), n, o=o, lse=lse)
+    hold(o, lse, s.oracle(), d)
+
+
+def test_empty_calls():
+    """No requests, no rows, a table without columns: nothing is written, or rows without keys."""
+    s = Step([(2, 30)], 4, 2, 64, 16, seed=1)
+    e = torch.empty((0,), dtype=torch.int32, device="cuda")
+    o, lse = torch.full((2, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 2), 7.0, device="cuda")
+    U.paged_attn_fwd(s.q, s.cache, i32([0]), e, e.view(0, 3), 1, o=o, lse=lse)
+    healthy()
+    assert torch.all(o == 7) and torch.all(lse == 7)
+    got = U.paged_attn_fwd(s.q[:0], s.cache, i32([0, 0]), i32([5]), i32([[0, 1]]), 1)
+    assert got[0].shape == (0, 4, 64) and got[1].shape == (4, 0)
+    U.kv_append(s.q[:0, :2], s.q[:0, :2], s.cache, e)
+    for max_q in (2, 20):
+        U.paged_attn_fwd(s.q, s.cache, i32([0, 2]), i32([32]), e.view(1, 0), max_q, o=o, lse=lse)
+        healthy()
+        assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
+        o.fill_(7.0)
+
+
+def test_more_heads_to_a_key_than_a_decode_tile():
+    """Groups of 17, 100 and 128 query heads: chunk units of a few tokens, of one token."""
+    for H, n in ((17, 20), (100, 3), (128, 5)):
+        s = Step([(n, 140), (1, 600)], H, 1, 64, 32, seed=H, pad=1)
+        s.check(max_q=n)
+
+
 # ------------------------------------------------------------------ streams, graphs, helpers
+
+def test_calls_follow_copies_and_other_kernels_of_their_stream():
+    """The calls' kernels may start before the kernel in front of them has ended; what they read was copied or
+    written right before them, and what they wrote is overwritten right behind them."""
+    a, b = Step([(1, 2000)] * 8, 8, 2, 128, 16, seed=21), Step([(1, 2000)] * 8, 8, 2, 128, 16, seed=22)
+    big = torch.empty(200 << 20, dtype=torch.uint8, device="cuda")
+    q, k, v = a.q.clone(), a.k.clone(), a.v.clone()
+    cache = U.PagedCache(k, v)
+    meta = [i32(a.cu), i32(a.kv), i32(a.table)]
+    other = [i32(b.cu), i32(b.kv), i32(b.table)]
+    want = [U.paged_attn_fwd(x.q, x.cache, *m, 1)[0].clone() for x, m in ((a, meta), (b, other))]
+    wantc = [U.paged_attn_fwd(x.q, x.cache, *m, 0)[0].clone() for x, m in ((a, meta), (b, other))]
+    o, lse = torch.empty_like(want[0]), torch.empty((8, 8), device="cuda")
+    ws = U.paged_attn_workspace(q, cache, 0)
+    out = []
+    for i in range(12):
+        x, m = ((a, meta), (b, other))[i & 1]
+        big.fill_(i)                                            # a kernel of some length in front
+        q.copy_(x.q)
+        k.copy_(x.k)
+        v.copy_(x.v)
+        U.paged_attn_fwd(q, cache, *m, (1, 0)[i % 3 == 0], o=o, lse=lse, workspace=ws)
+        out.append(o.clone())
+        o.fill_(float("nan"))
+    for i, got in enumerate(out):
+        assert torch.equal(got, (wantc if i % 3 == 0 else want)[i & 1]), i
+    healthy()
+
+
+def test_append_then_attention_without_a_pause():
+    """Each step's keys are written right before they are read: 40 decoding steps of one token in a row, the last
+    one against the oracle, every one against the same call made alone."""
+    H, Hkv, d, page, B = 8, 2, 128, 16, 3
+    s = Step([(1, 900), (1, 15), (1, 200)], H, Hkv, d, page, seed=31, width_extra=4, spare=12)
+    free = [p for p in range(s.cache.num_pages) if p not in set(s.table.reshape(-1))]
+    cached, new, table, fr, n_free = i32(s.kv), i32([1] * B), i32(s.table), i32(free), i32([len(free)])
+    ws = U.paged_attn_workspace(s.q, s.cache, 1)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    steps = [tuple(torch.randn((B, h, d), generator=g, device="cuda").to(torch.bfloat16) for h in (H, Hkv, Hkv)) for _ in range(40)]
+    torch.cuda.synchronize()
+    outs, states = [], []
+    for q, k, v in steps:
+        cu, kv, slots, info = U.page_plan(cached, new, fr, n_free, table, page, s.cache.num_pages, B)
+        U.kv_append(k, v, s.cache, slots)
+        outs.append(U.paged_attn_fwd(q, s.cache, cu, kv, table, 1, workspace=ws))
+        states.append((cu, kv))
+        cached = kv
+        n_free = n_free - info[1:2]
+    torch.cuda.synchronize()
+    for i, ((q, _, _), (cu, kv), (o, lse)) in enumerate(zip(steps, states, outs)):
+        again = U.paged_attn_fwd(q, s.cache, cu, kv, table, 1)   # later tokens lie behind kv: they are not seen
+        torch.cuda.synchronize()
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1]), i
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    ref = paged.paged_attention(f(steps[-1][0]), f(s.cache.k), f(s.cache.v), *(x.cpu().numpy() for x in states[-1]),
+                                table.cpu().numpy(), True)
+    hold(*outs[-1], ref, d)
+
+
+def test_two_graphs_share_a_workspace():
+    """A decoding graph and a mixed graph captured over one workspace and replayed in turn."""
+    a, b = Step([(1, 3000), (1, 40)], 8, 2, 128, 16, seed=41), Step([(150, 700), (1, 900), (0, 5)], 8, 2, 128, 16, seed=42)
+    ws = U.paged_attn_workspace(b.q, b.cache, 0)
+    calls = []
+    for x, max_q in ((a, 1), (b, 150)):
+        args = (x.q, x.cache, i32(x.cu), i32(x.kv), i32(x.table), max_q)
+        want = [t.clone() for t in U.paged_attn_fwd(*args)]
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            U.paged_attn_fwd(*args, o=o, lse=lse, workspace=ws)
+        calls.append((graph, o, lse, want, args))   # a graph reads its arguments where they were
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        graph, o, lse, want, _ = calls[i]
+        o.fill_(0)
+        graph.replay()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    healthy()
+
 
 def test_another_stream_and_two_at_once():
     """Two calls on two streams with their own workspaces, and one call whose outputs belong to a side stream."""
