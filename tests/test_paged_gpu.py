@@ -320,6 +320,43 @@ def test_many_requests(B, n, max_q):
     s.check(max_q=max_q)
 
 
+def _mixed_step(seed):
+    """60 requests of 8 key/value heads: too many units for one kernel, chunks among decoding and idle requests."""
+    rng = np.random.default_rng(seed)
+    reqs = [(0 if i % 13 == 6 else int(rng.integers(9, 70)) if i % 10 == 3 else 1, int(rng.integers(0, 300))) for i in range(60)]
+    return Step(reqs, 16, 8, 64, 16, seed=seed, pad=4)
+
+
+@pytest.mark.parametrize("mask,window", [("causal", 0), ("causal", 90), ("none", 0)])
+def test_mixed_batch_that_takes_both_kernels(mask, window):
+    s = _mixed_step(window)
+    s.check(max_q=70, mask=mask, window=window)
+    s.check(max_q=0, mask=mask, window=window)
+
+
+def test_both_kernels_follow_what_their_stream_wrote():
+    """The chunk kernel starts beside the decode kernel: both see what was written right before the call, and both are
+    done with it when what follows overwrites it."""
+    a, b = _mixed_step(1), _mixed_step(2)
+    want = [x.run(70) for x in (a, b)]
+    slots = []
+    for x in (a, b):
+        slots.append([x.q.clone(), x.k.clone(), x.v.clone(), i32(x.cu), i32(x.kv), i32(x.table)])
+    for i in range(10):
+        x, keep, (o0, l0) = ((a, slots[0], want[0]), (b, slots[1], want[1]))[i & 1]
+        q, k, v = (torch.full_like(t, float("nan")) for t in keep[:3])
+        big = torch.empty(100 << 20, dtype=torch.uint8, device="cuda").fill_(i)
+        for dst, src in zip((q, k, v), keep[:3]):
+            dst.copy_(src)
+        o, lse = torch.full_like(o0, 7.0), torch.full_like(l0, 7.0)
+        U.paged_attn_fwd(q, U.PagedCache(k, v), *keep[3:], 70, o=o, lse=lse)
+        for t in (q, k, v):
+            t.fill_(float("nan"))
+        assert torch.equal(o, o0) and torch.equal(lse, l0), i
+        del big
+    healthy()
+
+
 def test_keys_and_values_interleaved_in_one_allocation():
     """Pages that hold their keys and then their values: equal strides, neither tensor contiguous."""
     s = Step([(1, 300), (40, 77)], 8, 2, 128, 32, seed=3)
