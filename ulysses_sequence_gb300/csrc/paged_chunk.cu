@@ -11,9 +11,10 @@
 //             and V copies going; publishes each piece (a unit's part in this CTA) and each tile's
 //             missing pages;
 //   warp 1    MMA issuer: S_t = Q_t K^T into TMEM columns [128 t, 128 t + 128) and O_t += P_t V into
-//             [256 + 128 t, ...), P_t read from the first 64 columns of S_t as packed bf16 pairs;
-//   warps 2-5 softmax of tile 0, warps 6-9 of tile 1: thread i owns row i (TMEM lane i). It takes the
-//             row maximum, writes the weights over the scores, rescales O_t when the maximum grew by
+//             [256 + 128 t, ...), P_t read from the first 64 columns of S_t as packed bf16 pairs. The warp runs
+//             converged and one elected thread issues;
+//   warps 2-5 softmax of tile 0, warps 6-9 of tile 1: thread i owns row i (TMEM lane i). It takes the row's
+//             128 scores into registers, writes the weights over them, rescales O_t when the maximum grew by
 //             more than 2^8, and stores the row at the end of the unit, or leaves it as a piece.
 // One thread issues PV_t of a key tile before S_t of the next, and its tcgen05 operations complete in
 // order: when S_t of a key tile is there, the previous PV_t is over, so O_t may be rescaled and S_t's
@@ -21,6 +22,14 @@
 // they have read the previous piece's O_t.
 // Values behind a request's last key may be anything: in the tile that holds the end, warps 2-5 clear
 // those rows of V in shared memory before the product reads them (0 x NaN is NaN).
+//
+// What bounds it (32/8 heads of 128, 8192 new tokens over 16384 keys: 1000 us, 1.65 PFLOP/s, 0.86 of the
+// measured bf16 rate): a step of 256 rows and 128 keys takes 2970 cycles, of which the issuer spends 2100 on its
+// 32 MMAs, the tensor core's own rate, and 630 waiting for weights: a tile's chain softmax (1530) -> PV, S (1050)
+// is longer than the other tile's products. Tried and slower: one tile with three S buffers (the key/value
+// traffic doubles and the L2 bounds it: 1420 us); 64-key halves with two S buffers a tile (N = 64 products
+// cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); PV issued by
+// halves of P (no difference).
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -126,8 +135,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int cta = int(blockIdx.x);
     PagedWalk<kTile, kChunkUnitCost> w;
     int64_t* costs = reinterpret_cast<int64_t*>(smem);  // before the first copy
-    if (p.B <= kFewRequests) paged_costs<kTile, kChunkUnitCost, kChunkThreads>(p, costs);
-    else paged_share_block<kTile, kChunkUnitCost, kChunkThreads>(p, kChunkMinCost, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    if (p.B > kFewRequests)
+        paged_share_block<kTile, kChunkUnitCost, kChunkThreads>(p, kChunkMinCost, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
+    else if (p.B > kLaneRequests) paged_costs<kTile, kChunkUnitCost, kChunkThreads>(p, costs);
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -142,7 +152,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
+        if (p.B <= kLaneRequests) paged_share_lanes(p, kChunkMinCost, w);
+        else if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
         // a copy is one page (or 128 keys of a longer one) by 64 elements, or by the whole head where one
         // copy fills the tile; lane l copies page l / per, 64-element chunk l % per
         const int per = log_rows == 7 ? 1 : D / 64;

@@ -203,12 +203,11 @@ __device__ __forceinline__ bool paged_cut(PagedWalk<KT, OVH>& w, int min_cost, i
     return true;
 }
 
-// The walk's first unit, `rem` into request i: the head, then the row tile, 32 looked at at a time.
+// The walk's first unit, `rem` into request w.i, which is in w.s: the head, then the row tile, 32 looked at at
+// a time.
 template <int KT, int OVH>
-__device__ __forceinline__ void paged_start(const PagedParams& p, int i, int64_t rem, PagedWalk<KT, OVH>& w) {
+__device__ __forceinline__ void paged_start(const PagedParams& p, int64_t rem, PagedWalk<KT, OVH>& w) {
     const int lane = int(lane_id()), TQ = p.unit_tokens;
-    w.i = i;
-    w.s = paged_seq(p, i);
     w.t0 = 0;
     if (w.s.n <= TQ) {
         w.unit(p);
@@ -289,7 +288,37 @@ __device__ __forceinline__ bool paged_share_warp(const PagedParams& p, int min_c
 #pragma unroll 1
     while (i + 1 < p.B && rem >= costs[i]) rem -= costs[i++];
     fence_proxy_async_smem();
-    paged_start(p, i, rem, w);
+    w.i = i;
+    w.s = paged_seq(p, i);
+    paged_start(p, rem, w);
+    return true;
+}
+
+// The same for up to 32 requests, one to a lane, by one warp alone, without the barrier and the second look at the
+// request (one request of 1500 keys: 8.3 us against 8.7 us).
+constexpr int kLaneRequests = 32;
+template <int KT, int OVH>
+__device__ __forceinline__ bool paged_share_lanes(const PagedParams& p, int min_cost, PagedWalk<KT, OVH>& w) {
+    const int lane = int(lane_id());
+    PagedSeq s{};
+    if (lane < p.B) s = paged_seq(p, lane);
+    const int64_t mine = s.n > 0 ? paged_head_cost<KT, OVH>(p, s) * p.Hkv : int64_t(0);
+    int64_t incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    w.W = __shfl_sync(0xffffffffu, incl, 31);
+    int64_t begin;
+    if (!paged_cut(w, min_cost, begin)) return false;
+    const int64_t rem = begin - (incl - mine);
+    w.i = __ffs(__ballot_sync(0xffffffffu, rem >= 0 && rem < mine)) - 1;
+    w.s.start = __shfl_sync(0xffffffffu, s.start, w.i);
+    w.s.n = __shfl_sync(0xffffffffu, s.n, w.i);
+    w.s.kv = __shfl_sync(0xffffffffu, s.kv, w.i);
+    w.s.base = __shfl_sync(0xffffffffu, s.base, w.i);
+    paged_start(p, __shfl_sync(0xffffffffu, rem, w.i), w);
     return true;
 }
 
@@ -324,7 +353,9 @@ __device__ __forceinline__ bool paged_share_block(const PagedParams& p, int min_
         w.left = 0;
         return false;
     }
-    paged_start(p, int(sh[NW]), sh[NW + 1], w);
+    w.i = int(sh[NW]);
+    w.s = paged_seq(p, w.i);
+    paged_start(p, sh[NW + 1], w);
     return true;
 }
 
