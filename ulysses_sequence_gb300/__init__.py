@@ -501,176 +501,17 @@ def attn_bwd(q, k, v, o, lse, do, P: int, mask: Mask, layout: int = LAYOUT_TOKEN
 
 # ----------------------------------------------------------------------------- paged cache
 
-# The paged calls are small enough for the host's work to show: their checks are plain conditions, and a
-# message is put together only when one fails.
-
-def _call_stream(x, stream, where: str) -> int:
-    """The CUDA stream of one call on x's device, which must be the current one: the caller's, or the
-    current stream."""
-    import torch
-    device = x.get_device()
-    if device < 0:
-        raise ValueError(f"{where}: tensors must be on a CUDA device")
-    if device != torch._C._cuda_getDevice():
-        raise ValueError(f"{where}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)  # current_stream().cuda_stream without the objects
-    if stream.device != x.device:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {x.device}")
-    return stream.cuda_stream
+# The helpers of the paged key/value cache are in paged.py, which imports torch; they are brought in when one of
+# them is first asked for.
+_PAGED = ("PagedCache", "page_plan", "kv_append", "paged_attn_workspace", "paged_attn_fwd")
 
 
-def _new(shape, dtype, like, stream):
-    """An output allocated for the stream of the call, so that its memory is not reused before the call has run."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _check_tensor(x, shape, dtype, device: int, name: str, where: str) -> None:
-    """x is contiguous, of this shape and type, on the device of this index."""
-    if x.shape == shape and x.dtype is dtype and x.get_device() == device and x.is_contiguous():
-        return
-    raise ValueError(f"{where}: {name} must be contiguous {dtype} {tuple(shape)} on device {device}, got {x.dtype} "
-                     f"{tuple(x.shape)} with strides {x.stride()} on {x.device}")
-
-
-def _check_table(x, B: int, device: int, where: str) -> int:
-    """Row stride of an int32 block table [B][max_pages] with contiguous rows on this device."""
-    import torch
-    if (x.dtype is torch.int32 and x.dim() == 2 and x.shape[0] == B and x.get_device() == device
-            and (x.shape[1] < 2 or B == 0 or x.stride(1) == 1)):
-        return x.stride(0) if B > 1 else x.shape[1]
-    raise ValueError(f"{where}: block_table must be int32 [{B}][max_pages] with contiguous rows on device {device}, "
-                     f"got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
-
-
-def _check_rows(x, T: int, heads: int, d: int, device: int, name: str, where: str) -> int:
-    """Row stride of bf16 token rows [T][heads][d] whose rows are contiguous, on this device."""
-    import torch
-    if x.shape == (T, heads, d) and x.dtype is torch.bfloat16 and x.get_device() == device:
-        if T == 0:
-            return heads * d
-        row, head, one = x.stride()
-        if one == 1 and (heads == 1 or head == d):
-            return row if T > 1 else heads * d
-    raise ValueError(f"{where}: {name} must be bf16 [{T}][{heads}][{d}] with contiguous rows on device {device}, got "
-                     f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
-
-
-class PagedCache:
-    """A pool of key/value pages for the C ABI: k and v bf16 [num_pages][page_size][H_kv][d] with equal
-    strides and contiguous heads (any order of the first three dimensions in memory)."""
-
-    def __init__(self, k, v):
-        import torch
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
-            raise ValueError("PagedCache: k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
-        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.stride(3) != 1:
-            raise ValueError("PagedCache: k and v must be bf16 with contiguous heads")
-        if not k.is_cuda or k.device != v.device:
-            raise ValueError("PagedCache: k and v must be on one CUDA device")
-        self.k, self.v, self.device = k, v, k.get_device()
-        self.num_pages, self.page_size, self.H_kv, self.d = k.shape
-        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), *k.shape, k.stride(0), k.stride(1), k.stride(2))
-
-    @staticmethod
-    def empty(num_pages: int, page_size: int, H_kv: int, d: int, device="cuda") -> "PagedCache":
-        """A pool in the token layout, its contents undefined (unwritten entries are never used)."""
-        import torch
-        return PagedCache(*(torch.empty((num_pages, page_size, H_kv, d), dtype=torch.bfloat16, device=device)
-                            for _ in range(2)))
-
-
-def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size: int, num_pages: int, T: int, cu_q=None,
-              kv_lens=None, slot_map=None, info=None, stream=None):
-    """Block tables and slot maps of one step from request lengths, on the GPU (all int32): B requests hold
-    cached_lens[B] tokens and add new_lens[B]; new pages come from the end of free_pages[: n_free[0]] and
-    are written into block_table [B][max_pages] in place. Returns (cu_q [B+1], kv_lens [B], slot_map [T],
-    info [4] = rows planned, pages taken, pages missing, tokens dropped). The list is not changed:
-    ``n_free -= info[1:2]`` keeps the pages."""
-    import torch
-    where, B, dev, i32 = "page_plan", block_table.shape[0], block_table.get_device(), torch.int32
-    table_stride = _check_table(block_table, B, dev, where)
-    _check_tensor(cached_lens, (B,), i32, dev, "cached_lens", where)
-    _check_tensor(new_lens, (B,), i32, dev, "new_lens", where)
-    _check_tensor(n_free, (1,), i32, dev, "n_free", where)
-    _check_tensor(free_pages, (free_pages.numel(),), i32, dev, "free_pages", where)
-    st = _call_stream(block_table, stream, where)
-    outs = []
-    for name, x, n in (("cu_q", cu_q, B + 1), ("kv_lens", kv_lens, B), ("slot_map", slot_map, T), ("info", info, 4)):
-        if x is None:
-            x = _new((n,), i32, block_table, stream)
-        else:
-            _check_tensor(x, (n,), i32, dev, name, where)
-        outs.append(x)
-    cu_q, kv_lens, slot_map, info = outs
-    check(load().ulysses_page_plan(B, T, page_size, block_table.shape[1], table_stride, num_pages, cached_lens.data_ptr(),
-                                   new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                                   block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slot_map.data_ptr(),
-                                   info.data_ptr(), st), where)
-    return cu_q, kv_lens, slot_map, info
-
-
-def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
-    """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
-    fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
-    import torch
-    where, T, dev = "kv_append", k.shape[0], cache.device
-    k_stride = _check_rows(k, T, cache.H_kv, cache.d, dev, "k", where)
-    v_stride = _check_rows(v, T, cache.H_kv, cache.d, dev, "v", where)
-    _check_tensor(slot_map, (T,), torch.int32, dev, "slot_map", where)
-    check(load().ulysses_kv_append(ctypes.byref(cache.struct), T, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-                                   slot_map.data_ptr(), _call_stream(cache.k, stream, where)), where)
-
-
-def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
-    """Workspace of paged_attn_fwd for q [T][H][d]; its size depends on H, d and max_q alone, so one serves every
-    step of a program. Calls that may overlap on the GPU need one each."""
-    import torch
-    n = ulysses_paged_attn_workspace_size(q.shape[1], cache.H_kv, cache.d, max_q)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-
-
-def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int = 0, mask: Optional[Mask] = None,
-                   window: int = 0, scale: float = 0.0, o=None, lse=None, workspace=None, stream=None):
-    """Attention of packed new tokens q bf16 [T][H][d] (request i owns rows cu_q[i] .. cu_q[i+1]) over the pages that
-    block_table [B][max_pages] names, kv_lens[B] keys each, the new tokens last. mask: Mask.causal() (the default)
-    by position, with an optional sliding window, or Mask.none(). max_q bounds the new tokens of a request where
-    known (1 when decoding; 0: unknown). Returns (o bf16 [T][H][d], lse fp32 [H][T]); rows behind the last
-    request are left as they were."""
-    import torch
-    where, dev = "paged_attn_fwd", cache.device
-    if q.dim() != 3:
-        raise ValueError(f"{where}: q must be [T][H][d], got {tuple(q.shape)}")
-    T, H, d = q.shape
-    B = block_table.shape[0]
-    q_stride = _check_rows(q, T, H, cache.d, dev, "q", where)
-    table_stride = _check_table(block_table, B, dev, where)
-    _check_tensor(cu_q, (B + 1,), torch.int32, dev, "cu_q", where)
-    _check_tensor(kv_lens, (B,), torch.int32, dev, "kv_lens", where)
-    st = _call_stream(q, stream, where)
-    if o is None:
-        o = _new((T, H, d), torch.bfloat16, q, stream)
-    else:
-        _check_tensor(o, (T, H, d), torch.bfloat16, dev, "o", where)
-    if lse is None:
-        lse = _new((H, T), torch.float32, q, stream)
-    else:
-        _check_tensor(lse, (H, T), torch.float32, dev, "lse", where)
-    if workspace is None:
-        n = ulysses_paged_attn_workspace_size(H, cache.H_kv, d, max_q)
-        workspace = _new((max(n, 256),), torch.uint8, q, stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"{where}: workspace must be contiguous on device {dev}")
-    check(load().ulysses_paged_attn_fwd(ctypes.byref(cache.struct), B, T, H, max_q,
-                                        MASK_CAUSAL if mask is None else mask.kind, window, scale, q.data_ptr(), q_stride,
-                                        cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), table_stride,
-                                        block_table.shape[1], o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), st), where)
-    return o, lse
+def __getattr__(name: str):
+    if name in _PAGED:
+        from . import paged
+        globals().update((n, getattr(paged, n)) for n in _PAGED)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def shutdown() -> None:

@@ -115,9 +115,10 @@ bool encode_memo(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, con
         k.estr[i] = estr[i];
         if (i + 1 < rank) k.strides[i] = strides[i];
     }
-    uint64_t h = 1469598103934665603ull;  // FNV-1a over the key's bytes
-    const unsigned char* kb = reinterpret_cast<const unsigned char*>(&k);
-    for (size_t i = 0; i < sizeof(k); ++i) h = (h ^ kb[i]) * 1099511628211ull;
+    static_assert(sizeof(MapKey) % 8 == 0, "hashed by words");
+    uint64_t h = 1469598103934665603ull, words[sizeof(MapKey) / 8];  // FNV-1a by the key's 64-bit words
+    std::memcpy(words, &k, sizeof(k));
+    for (uint64_t word : words) h = ((h ^ word) * 1099511628211ull) ^ (h >> 29);
     MapSlot& sl = t_maps[(h ^ (h >> 32)) & 63];
     if (sl.valid && std::memcmp(&sl.key, &k, sizeof(k)) == 0) {
         *map = sl.map;

@@ -51,8 +51,8 @@ static int launch_join(const PagedParams& p, const PagedParts& decode, const Pag
 size_t paged_attn_workspace_bytes(int H, int H_kv, int d_h, int max_q) {
     const int G = H / H_kv;
     size_t decode = 0, chunk = 0;
-    if (decode_fits(G)) paged_decode_parts(nullptr, d_h, &decode);
-    if (!decode_only(G, max_q)) paged_chunk_parts(nullptr, d_h, &chunk);
+    if (decode_fits(G)) paged_decode_parts(nullptr, d_h, 0, &decode);
+    if (!decode_only(G, max_q)) paged_chunk_parts(nullptr, d_h, 0, &chunk);
     return decode + chunk;
 }
 
@@ -71,16 +71,16 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.err = device_error_word();
     if (!p.err) return ULYSSES_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const int d = a.cache.d_h;
+    const int d = a.cache.d_h, sms = device_sm_count();
     const bool only = decode_only(p.G, a.max_q);
     PagedParts decode{}, chunk{};
     size_t bytes = 0;
-    const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > 3 * device_sm_count();
+    const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > 3 * sms;
     p.min_rows = 1;
     if (only || both) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
         p.unit_tokens = paged_decode_rows() / p.G;
-        p.parts = decode = paged_decode_parts(ws, d, &bytes);
+        p.parts = decode = paged_decode_parts(ws, d, sms, &bytes);
         const int rc = launch_paged_decode(a, p, stream);
         if (rc != ULYSSES_OK) return rc;
         p.min_rows = paged_decode_rows() + 1;
@@ -88,7 +88,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     if (!only) {
         p.max_rows = 0x7fffffff;
         p.unit_tokens = 2 * (kTile / p.G);
-        p.parts = chunk = paged_chunk_parts(ws + bytes, d, &bytes);
+        p.parts = chunk = paged_chunk_parts(ws + bytes, d, sms, &bytes);
         const int rc = launch_paged_chunk(a, p, both, stream);
         if (rc != ULYSSES_OK) return rc;
     }

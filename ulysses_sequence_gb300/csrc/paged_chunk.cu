@@ -526,8 +526,8 @@ int launch_chunk_d(const PagedAttnArgs& a, const PagedParams& p, bool behind_dec
 
 }  // namespace
 
-PagedParts paged_chunk_parts(void* workspace, int d_h, size_t* bytes) {
-    return paged_parts(workspace, kChunkMaxCtas, std::min(device_sm_count(), kChunkMaxCtas), kChunkRows, d_h, bytes);
+PagedParts paged_chunk_parts(void* workspace, int d_h, int sms, size_t* bytes) {
+    return paged_parts(workspace, kChunkMaxCtas, sms, kChunkRows, d_h, bytes);
 }
 
 int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream) {

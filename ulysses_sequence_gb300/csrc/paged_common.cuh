@@ -421,11 +421,11 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const PagedParams p, con
 // of `rows` tokens of one page and head by `chunks` chunks (chunk after chunk), 128-byte swizzle.
 bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks);
 
-// Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu). p.parts is filled in; the
-// workspace sizes are those of each kernel's pieces.
+// Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu): where their pieces lie in a
+// workspace on a device of `sms` SMs (`bytes` of it, whatever the device), and their launches.
 int paged_decode_rows();
-PagedParts paged_decode_parts(void* workspace, int d_h, size_t* bytes);
-PagedParts paged_chunk_parts(void* workspace, int d_h, size_t* bytes);
+PagedParts paged_decode_parts(void* workspace, int d_h, int sms, size_t* bytes);
+PagedParts paged_chunk_parts(void* workspace, int d_h, int sms, size_t* bytes);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
 int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream);
 
@@ -440,7 +440,7 @@ inline PagedParts paged_parts(void* workspace, int most, int ctas, int rows, int
     w.meta = reinterpret_cast<PagedMeta*>(ws + at);
     at += size_t(most) * sizeof(PagedMeta);
     w.rows = rows;
-    w.ctas = ctas;
+    w.ctas = ctas < most ? ctas : most;
     *bytes = (at + 255) / 256 * 256;
     return w;
 }

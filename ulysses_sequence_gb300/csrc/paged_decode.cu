@@ -414,8 +414,8 @@ int launch_decode_d(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t s
 
 int paged_decode_rows() { return kDecodeRows; }
 
-PagedParts paged_decode_parts(void* workspace, int d_h, size_t* bytes) {
-    return paged_parts(workspace, kDecodeMaxCtas, std::min(2 * device_sm_count(), kDecodeMaxCtas), kDecodeRows, d_h, bytes);
+PagedParts paged_decode_parts(void* workspace, int d_h, int sms, size_t* bytes) {
+    return paged_parts(workspace, kDecodeMaxCtas, 2 * sms, kDecodeRows, d_h, bytes);
 }
 
 int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream) {
