@@ -231,6 +231,15 @@ def test_a_single_tile_long_context_splits_over_the_grid():
         s.check(max_q=n)
 
 
+@pytest.mark.parametrize("H,d,n", [(32, 128, 6), (32, 64, 6), (16, 128, 70), (16, 64, 70)])
+def test_many_key_tiles_in_a_row(H, d, n):
+    """Units of one and of two row tiles with twenty and more key tiles to a CTA, in batches that fill the grid."""
+    rng = np.random.default_rng(H + d + n)
+    reqs = [(n, int(c)) for c in rng.integers(1800, 3000, 20 if n < 10 else 3)]
+    s = Step(reqs, H, 8, d, 64, seed=d + n)
+    s.check(max_q=n)
+
+
 def test_rows_that_see_nothing():
     """Lengths below the number of new tokens: early rows have negative positions. Lengths of zero: no keys."""
     for max_q, H, Hkv in ((1, 4, 2), (20, 4, 2), (0, 8, 1)):
