@@ -28,7 +28,8 @@
 // 32 MMAs, the tensor core's own rate, and 630 waiting for weights: a tile's chain softmax (1530) -> PV, S (1050)
 // is longer than the other tile's products. Tried and slower: one tile with three S buffers (the key/value
 // traffic doubles and the L2 bounds it: 1420 us); 64-key halves with two S buffers a tile (N = 64 products
-// cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); PV issued by
+// cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); score buffers
+// that rotate (1100 us; with the third one that d = 64 has room for, 770 us against 850 us there); PV issued by
 // halves of P (no difference).
 #include <algorithm>
 
