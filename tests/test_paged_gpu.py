@@ -90,6 +90,15 @@ def test_plan_strided_table_and_large_lengths():
     assert torch.all(wide[:, :2] == 7) and torch.all(wide[:, 6:] == 7)
 
 
+@pytest.mark.parametrize("cached", [2 ** 31 - 4096, 2 ** 31 - 4106, 2 ** 31 - 9000])
+def test_plan_up_to_the_last_token_of_31_bits(cached):
+    """The largest table and T that are taken together: max_pages * page_size + T = 2^31 - 1."""
+    page, width = 4096, 2 ** 19 - 1
+    table = np.full((1, width), -1)
+    table[0, : -(-cached // page)] = 5
+    run_plan([cached], [4095], [9, 8, 7], 3, table, page, 10, 4095)
+
+
 # ------------------------------------------------------------------ kv_append
 
 @pytest.mark.parametrize("T,H,d,page,head_major,fused", [(1, 1, 8, 16, False, False), (5, 3, 64, 16, True, True),

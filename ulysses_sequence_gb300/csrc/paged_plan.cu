@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     grid_release();
     const int page = 1 << p.page_shift;
     const int cap = p.max_pages << p.page_shift;
+    // pages of n tokens: n may be 2^31 - 1, so the sum is unsigned
+    auto pages_of = [&](int n) { return int((uint32_t(n) + uint32_t(page - 1)) >> p.page_shift); };
     const int n_free = min(max(*p.n_free, 0), p.free_capacity);
 
     for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     scan_array(cu, p.B, uint32_t(p.T), warp_sums);
     for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
         const int c = held[i], kv = c + cu[i + 1] - cu[i];
-        pg[i] = min((kv + page - 1) >> p.page_shift, p.max_pages) - ((c + page - 1) >> p.page_shift);
+        pg[i] = min(pages_of(kv), p.max_pages) - pages_of(c);
     }
     __syncthreads();
     scan_array(pg, p.B, 0x7fffffffu, warp_sums);
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
         if (t < rows) {
             const int i = owner(cu, p.B, int(t));
             const int c = held[i], pos = c + int(t) - cu[i], at = pos >> p.page_shift;
-            const int has = (c + page - 1) >> p.page_shift;
+            const int has = pages_of(c);
             if (at < p.max_pages) {
                 const int id = at < has ? p.table[i * p.table_stride + at] : taken(pg[i] + at - has);
                 if (unsigned(id) < unsigned(p.num_pages)) slot = (id << p.page_shift) + (pos & (page - 1));
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     for (int64_t x = first; x < pages; x += step) {
         const int i = owner(pg, p.B, int(x));
-        const int has = (held[i] + page - 1) >> p.page_shift;
+        const int has = pages_of(held[i]);
         p.table[i * p.table_stride + has + (int(x) - pg[i])] = taken(int(x));
     }
     if (blockIdx.x != 0) return;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     unsigned long long asked = 0;
     for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
         const int kv = held[i] + cu[i + 1] - cu[i];
-        beyond += max(0, ((kv + page - 1) >> p.page_shift) - p.max_pages);
+        beyond += max(0, pages_of(kv) - p.max_pages);
         asked += static_cast<unsigned long long>(max(p.fresh[i], 0));
     }
     __shared__ int sh_beyond;
