@@ -249,6 +249,14 @@ def test_many_key_tiles_in_a_row(H, d, n):
     s.check(max_q=n)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_of_one_and_of_two_tiles_in_turn(d):
+    """Every CTA walks units of one row tile among units of two, each of several key tiles."""
+    rng = np.random.default_rng(d)
+    reqs = [(int(rng.integers(5, 33)) if i % 3 else int(rng.integers(40, 65)), int(rng.integers(0, 900))) for i in range(260)]
+    Step(reqs, 8, 2, d, 32, seed=d).check()
+
+
 def test_rows_that_see_nothing():
     """Lengths below the number of new tokens: early rows have negative positions. Lengths of zero: no keys."""
     for max_q, H, Hkv in ((1, 4, 2), (20, 4, 2), (0, 8, 1)):

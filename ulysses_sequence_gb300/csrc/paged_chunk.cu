@@ -10,16 +10,22 @@
 //   warp 0    producer: walks the share, looks up the pages (one lane per page copy) and keeps the Q, K
 //             and V copies going; publishes each piece (a unit's part in this CTA) and each tile's
 //             missing pages;
-//   warp 1    MMA issuer: S_t = Q_t K^T into TMEM columns [128 t, 128 t + 128) and O_t += P_t V into
-//             [256 + 128 t, ...), P_t read from the first 64 columns of S_t as packed bf16 pairs. The warp runs
-//             converged and one elected thread issues;
+//   warp 1    MMA issuer: S_t = Q_t K^T into a 128-column buffer of TMEM and O_t += P_t V into columns of its own, P_t
+//             read from the first 64 columns of S_t's buffer as packed bf16 pairs. The warp runs converged and one
+//             elected thread issues;
 //   warps 2-5 softmax of tile 0, warps 6-9 of tile 1: thread i owns row i (TMEM lane i). It takes the row's
 //             128 scores into registers, writes the weights over them, rescales O_t when the maximum grew by
 //             more than 2^8, and stores the row at the end of the unit, or leaves it as a piece.
-// One thread issues PV_t of a key tile before S_t of the next, and its tcgen05 operations complete in
-// order: when S_t of a key tile is there, the previous PV_t is over, so O_t may be rescaled and S_t's
-// columns reused. A piece's first PV_t waits for that tile's weights, which its warps write only after
-// they have read the previous piece's O_t.
+// One thread issues all products, and its tcgen05 operations complete in order.
+// d = 128: S_t has buffer t, and PV_t of a key tile is issued before S_t of the next: when that is there, the
+// previous PV_t is over, so O_t may be rescaled and S_t's columns reused.
+// d = 64 (AHEAD): O leaves room for a third S buffer. The scores, in the order of their issue, take the three in turn,
+// and S_t of a key tile is issued before PV_t of the one before, so that it is ready when that one's weights
+// are done (8192 new tokens over 16384 keys, 32/8 heads: 760 us, against 855 us with two buffers). The buffer
+// it takes held weights whose product is issued before it. O_t is rescaled once PV_t of the key tile before has
+// completed. A fast warp may be one key tile ahead of its tile's others, hence two barriers by parity.
+// A piece's first PV_t waits for that tile's weights, which its warps write only after they have read the
+// previous piece's O_t.
 // Values behind a request's last key may be anything: in the tile that holds the end, warps 2-5 clear
 // those rows of V in shared memory before the product reads them (0 x NaN is NaN).
 //
@@ -28,9 +34,9 @@
 // 32 MMAs, the tensor core's own rate, and 630 waiting for weights: a tile's chain softmax (1530) -> PV, S (1050)
 // is longer than the other tile's products. Tried and slower: one tile with three S buffers (the key/value
 // traffic doubles and the L2 bounds it: 1420 us); 64-key halves with two S buffers a tile (N = 64 products
-// cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); score buffers
-// that rotate (1100 us; with the third one that d = 64 has room for, 770 us against 850 us there); PV issued by
-// halves of P (no difference).
+// cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); PV issued by
+// halves of P (no difference). d = 64, P in columns of its own so that both tiles' scores come a key tile
+// ahead: 980 us, both tiles' weights are then computed at once and neither's beside the products.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -50,7 +56,6 @@ template <int D>
 struct ChunkCfg {
     static constexpr int NSK = D == 64 ? 6 : 3;  // K and V pipeline stages
     static constexpr int NSV = D == 64 ? 6 : 2;
-    static_assert(NSK + 1 < kInfoRing, "tile descriptions outlive their readers");
     static constexpr uint32_t TILE_BYTES = kTile * D * 2;
     static constexpr uint32_t CHUNK_BYTES = kTile * 128;  // 128 rows x 64 elements, swizzled
     static constexpr uint32_t OFF_K = 2 * TILE_BYTES;
@@ -61,7 +66,11 @@ struct ChunkCfg {
     static constexpr uint32_t OFF_BAR = OFF_SH + 128;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 512 + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
-    static constexpr uint32_t TMEM_COLS = 512;  // S0 | S1 | O0 | O1
+    // TMEM: S buffers, O0, O1. d = 64 leaves room for a third S buffer.
+    static constexpr bool AHEAD = D == 64;
+    static constexpr uint32_t COL_O = (AHEAD ? 3 : 2) * kTile, TMEM_COLS = 512;
+    static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory");
+    static_assert(NSK + (AHEAD ? 2 : 1) <= kInfoRing, "tile descriptions outlive their readers");
 };
 
 // A unit's part in one CTA, as the producer describes it to the other warps.
@@ -96,9 +105,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* k_empty = k_full + NSK;       // [NSK]
     uint64_t* v_full = k_empty + NSK;       // [NSV]
     uint64_t* v_empty = v_full + NSV;       // [NSV]
-    uint64_t* s_full = v_empty + NSV;       // [2]
-    uint64_t* p_full = s_full + 2;          // [2]
-    uint64_t* o_done = p_full + 2;          // [2]
+    uint64_t* s_full = v_empty + NSV;       // [2][2], by tile; with AHEAD by parity of its key tiles too
+    uint64_t* p_full = s_full + 4;          // [2][2], the same
+    uint64_t* o_done = p_full + 4;          // [2], by tile: a piece's products, with AHEAD a key tile's
     uint64_t* piece_full = o_done + 2;      // [2]
     uint64_t* piece_empty = piece_full + 2; // [2], MMA issuer and eight softmax warps
     uint64_t* info_full = piece_empty + 2;  // [kInfoRing]
@@ -119,9 +128,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_init(v_full + i, 1);
             mbar_init(v_empty + i, 1);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+        }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full + t, 1);
-            mbar_init(p_full + t, 4);
             mbar_init(o_done + t, 1);
             mbar_init(piece_full + t, 1);
             mbar_init(piece_empty + t, 9);
@@ -132,6 +143,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         fence_mbar_init();
     }
     const int TOK = p.unit_tokens / 2;  // tokens of a tile
+    // place and phase of the barriers of tile t's c-th key tile
+    auto tile_bar = [](uint64_t* bars, int t, int c) { return bars + (C::AHEAD ? 2 * t + (c & 1) : t); };
+    auto tile_phase = [](int c) { return uint32_t(C::AHEAD ? c >> 1 : c) & 1u; };
+    auto next_buffer = [](int b, int by) { return b + by < 3 ? b + by : b + by - 3; };  // AHEAD
     if (!behind_decode) grid_wait();
     const int cta = int(blockIdx.x);
     PagedWalk<kTile, kChunkUnitCost> w;
@@ -271,24 +286,31 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
             constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
             const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
-            auto issue_s = [&](int t, int sk) {  // S_t = Q_t K^T
+            bool ok = true;
+            int j = 0;                          // key tiles so far
+            int s0 = 0, s1 = 0, c0 = 0, c1 = 0; // S_t and PV_t so far
+            int bs = 0, bp = 0;                 // AHEAD: S buffer of the next S and of the next PV
+            auto issue_s = [&](int t, int sk, int& c) {  // S_t = Q_t K^T
                 const uint64_t dq = sdesc_sw128(aQ + t * C::TILE_BYTES, 16, 1024);
                 const uint64_t dk = sdesc_sw128(aK + sk * C::TILE_BYTES, 16, 1024);
+                const uint32_t col = kTile * (C::AHEAD ? bs : t);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t o = (k >> 2) * C::CHUNK_BYTES + (k & 3) * 32;
-                    umma_ss_one(one, 128 * t, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
+                    umma_ss_one(one, col, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
                 }
-                umma_commit_one(one, s_full + t);
+                umma_commit_one(one, tile_bar(s_full, t, c++));
+                bs = next_buffer(bs, 1);
             };
-            auto issue_pv = [&](int t, int sv, bool first) {  // O_t (+)= P_t V
+            auto issue_pv = [&](int t, int sv, bool first, bool last) {  // O_t (+)= P_t V
                 const uint64_t dv = sdesc_sw128(aV + sv * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
+                const uint32_t col = kTile * (C::AHEAD ? bp : t);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)  // 16 keys = 8 TMEM columns of P per step
-                    umma_ts_one(one, 256 + 128 * t, 128 * t + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
+                    umma_ts_one(one, C::COL_O + D * t, col + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
+                if (C::AHEAD || last) umma_commit_one(one, o_done + t);
+                bp = next_buffer(bp, 1);
             };
-            bool ok = true;
-            int j = 0, c0 = 0, c1 = 0;  // key tiles so far, PV_t so far
             for (int piece = 0; ok; ++piece) {
                 if (!(ok = wait(piece_full + (piece & 1), (piece >> 1) & 1, 1))) break;
                 const int n = pieces[piece & 1].tiles;
@@ -299,30 +321,35 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!(ok = wait(q_full, piece & 1, 2))) break;
                 if (!(ok = wait(k_full + j % NSK, (j / NSK) & 1, 3))) break;
                 tc_fence_after();
-                issue_s(0, j % NSK);
-                if (two) issue_s(1, j % NSK);
+                issue_s(0, j % NSK, s0);
+                if (two) issue_s(1, j % NSK, s1);
                 umma_commit_one(one, k_empty + j % NSK);
                 if (n == 1) umma_commit_one(one, q_empty);
                 for (int i = 0; i < n; ++i, ++j) {
                     const bool next = i + 1 < n;
                     const int sv = j % NSV, sk = (j + 1) % NSK;
-                    if (!(ok = wait(v_full + sv, (j / NSV) & 1, 4))) break;
-                    if (!(ok = wait(p_full, c0++ & 1, 5))) break;
-                    tc_fence_after();
-                    issue_pv(0, sv, i == 0);
-                    if (next) {
+                    if (C::AHEAD && next) {
                         if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
                         tc_fence_after();
-                        issue_s(0, sk);
-                    } else {
-                        umma_commit_one(one, o_done);
+                        issue_s(0, sk, s0);
+                    }
+                    if (!(ok = wait(v_full + sv, (j / NSV) & 1, 4))) break;
+                    if (!(ok = wait(tile_bar(p_full, 0, c0), tile_phase(c0), 5))) break;
+                    ++c0;
+                    tc_fence_after();
+                    issue_pv(0, sv, i == 0, !next);
+                    if (!C::AHEAD && next) {
+                        if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
+                        tc_fence_after();
+                        issue_s(0, sk, s0);
                     }
                     if (two) {
-                        if (!(ok = wait(p_full + 1, c1++ & 1, 7))) break;
+                        if (C::AHEAD && next) issue_s(1, sk, s1);
+                        if (!(ok = wait(tile_bar(p_full, 1, c1), tile_phase(c1), 7))) break;
+                        ++c1;
                         tc_fence_after();
-                        issue_pv(1, sv, i == 0);
-                        if (next) issue_s(1, sk);
-                        else umma_commit_one(one, o_done + 1);
+                        issue_pv(1, sv, i == 0, !next);
+                        if (!C::AHEAD && next) issue_s(1, sk, s1);
                     }
                     if (next) umma_commit_one(one, k_empty + sk);
                     if (i + 2 == n) umma_commit_one(one, q_empty);  // the piece's last scores are under way
@@ -340,10 +367,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int wq = warp & 3;                  // TMEM lane quadrant of this warp
         const int row = wq * 32 + lane;           // row within the tile (TMEM lane)
         const uint32_t lane_off = uint32_t(wq * 32) << 16;
-        const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + 256 + 128 * t + lane_off;
+        uint32_t tS = tmem + kTile * t + lane_off;
+        const uint32_t tO = tmem + C::COL_O + D * t + lane_off;
         const int tok = row / p.G;                // the row's token within the tile
         bool ok = true;
         int j = 0, cs = 0, units = 0;             // key tiles so far; this tile's S and O so far
+        int buffer0 = 0;                          // AHEAD: S buffer of the piece's first scores
         for (int piece = 0; ok; ++piece) {
             ok = __all_sync(0xffffffffu, mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
             if (!ok) break;
@@ -359,13 +388,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (u.tokens <= t * TOK) {  // the unit has one tile
                 done_with_piece();
                 j += tiles;
+                if (C::AHEAD) buffer0 = next_buffer(buffer0, tiles % 3);
                 continue;
+            }
+            int width = 0, buffer = 0;                // AHEAD: tiles of the unit, S buffer
+            if (C::AHEAD) {
+                width = u.tokens > TOK ? 2 : 1;
+                buffer = next_buffer(buffer0, t);
+                buffer0 = next_buffer(buffer0, width * tiles % 3);
             }
             const int kv = u.kv;
             int key0 = u.key0;
             float m_used = -INFINITY, l_sum = 0.f;  // running maximum (log2 domain) and sum
             for (int i = 0; i < tiles; ++i, ++j, key0 += kTile) {
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, cs++ & 1, ab, ROLE_SOFTMAX, 2) &&
+                const int c = cs++;
+                if (C::AHEAD) tS = tmem + kTile * buffer + lane_off;
+                ok = __all_sync(0xffffffffu, mbar_wait(tile_bar(s_full, t, c), tile_phase(c), ab, ROLE_SOFTMAX, 2) &&
                                                  mbar_wait(info_full + j % kInfoRing, (j / kInfoRing) & 1, ab, ROLE_SOFTMAX, 3));
                 if (!ok) break;
                 tc_fence_after();
@@ -415,6 +453,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 rs4[0] = add2(add2(rs4[0], rs4[1]), add2(rs4[2], rs4[3]));
                 const float rs = rs4[0].x + rs4[0].y;
                 l_sum = l_sum * alpha + rs;
+                if (C::AHEAD && i > 0) {
+                    // O_t holds still between the product of the key tile before and this one's
+                    ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, units++ & 1, ab, ROLE_SOFTMAX, 5));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (i > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
                     for (int x = 0; x < D / 32; ++x) {
@@ -443,7 +487,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + t);
+                if (lane == 0) mbar_arrive(tile_bar(p_full, t, c));
+                if (C::AHEAD) buffer = next_buffer(buffer, width);
             }
             if (!ok) break;
             // -------------------------------------------------------------- the piece's rows
