@@ -648,3 +648,20 @@ def test_helpers_refuse_what_the_kernels_cannot_read():
     k = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         U.kv_append(k, k.cpu(), s.cache, i32([0, 1]))
+
+
+def test_helpers_refuse_sizes_past_32_bits():
+    """The library's sizes are 32-bit: a larger one is refused, not taken by its low bits."""
+    s = Step([(2, 30)], 4, 2, 64, 16, seed=1)
+    ok = dict(q=s.q, cache=s.cache, cu_q=i32(s.cu), kv_lens=i32(s.kv), block_table=i32(s.table))
+    for bad in (dict(window=2 ** 32 + 1), dict(max_q=2 ** 32 + 1), dict(window=-2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            U.paged_attn_fwd(**{**ok, **bad})
+    U.paged_attn_fwd(**ok, window=2 ** 31 - 1, max_q=2 ** 31 - 1)
+    with pytest.raises(ValueError):
+        U.paged_attn_workspace(s.q, s.cache, 2 ** 32)
+    one = i32([1])
+    for sizes in ((16, 10, -1), (16, 2 ** 32 + 10, 1), (2 ** 32 + 16, 10, 1), (16, 10, 2 ** 32)):
+        with pytest.raises(ValueError):
+            U.page_plan(one, one, one, one, i32([[0, -1]]), *sizes)
+    healthy()

@@ -23,6 +23,7 @@ import torch
 import ulysses_sequence_gb300 as U
 
 _I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_INT_MAX = 2 ** 31 - 1  # of the C ABI's int arguments, which ctypes would wrap
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without the objects
 
@@ -105,6 +106,8 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     info [4] = rows planned, pages taken, pages missing, tokens dropped). The list is not changed:
     ``n_free -= info[1:2]`` keeps the pages."""
     where = "page_plan"
+    if not (0 <= T <= _INT_MAX and -1 <= num_pages <= _INT_MAX and -1 <= page_size <= _INT_MAX):
+        raise ValueError(f"{where}: T, num_pages and page_size must fit 32 bits, got {T}, {num_pages}, {page_size}")
     B, width = block_table.shape
     dev = block_table.get_device()
     table_stride = _table_stride(block_table, B, dev, where)
@@ -165,6 +168,8 @@ def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
 def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
     """Workspace of paged_attn_fwd for q [T][H][d]; its size depends on H, d and max_q alone, so one serves every
     step of a program. Calls that may overlap on the GPU need one each."""
+    if not -1 <= max_q <= _INT_MAX:
+        raise ValueError(f"paged_attn_workspace: max_q must fit 32 bits, got {max_q}")
     n = U.ulysses_paged_attn_workspace_size(q.shape[1], cache.H_kv, cache.d, max_q)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
@@ -177,6 +182,8 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
     known (1 when decoding; 0: unknown). Returns (o bf16 [T][H][d], lse fp32 [H][T]); rows behind the last
     request are left as they were."""
     where, dev = "paged_attn_fwd", cache.device
+    if not (-1 <= window <= _INT_MAX and -1 <= max_q <= _INT_MAX):
+        raise ValueError(f"{where}: window and max_q must fit 32 bits, got {window}, {max_q}")
     if q.dim() != 3:
         raise ValueError(f"{where}: q must be [T][H][d], got {tuple(q.shape)}")
     T, H, d = shape = q.shape
