@@ -338,7 +338,8 @@ int ulysses_kv_append(const ulysses_kv_cache_t *cache, int T, const void *k, int
  * used, NaN and infinities included; K and V of tokens below kv_lens[i] must be finite where V's
  * weight is zero. Query head h attends with key/value head h / (H / H_kv).
  * q: [T][H][d_h] bf16, rows q_stride elements apart (a multiple of 8, at least H * d_h);
- * o: [T][H][d_h] bf16; lse: [H][T] fp32. A row with no permitted key gets o = 0 and lse = -inf.
+ * o: [T][H][d_h] bf16; lse: [H][T] fp32. A row with no permitted key gets o = 0 and lse = -inf; one
+ * with a NaN among its scores gets NaN in both.
  * max_q: an upper bound of n_i where the caller knows one (1 when decoding), else 0: it chooses
  * the kernels, and the results are right whatever it says. softmax_scale <= 0 selects
  * 1 / sqrt(d_h). Row starts must ascend; ones outside [0, T] are clamped, lengths to [0, 2^30].

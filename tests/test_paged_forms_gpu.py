@@ -1,6 +1,6 @@
 """More of the paged-cache calls on the GPU, held to the oracle and the bounds of test_paged_gpu.py: the wide copy of
-kv_append, masks in the decode kernel, both kernels with heads of 128, a step that a graph captures first, and a
-served block with requests that pause and finish."""
+kv_append, masks in the decode kernel, both kernels with heads of 128, scores that are NaN, a step that a graph
+captures first, and a served block with requests that pause and finish."""
 
 import subprocess
 import sys
@@ -77,6 +77,31 @@ def test_both_kernels_with_heads_of_128(mask, window):
     reqs = [(0 if i % 13 == 6 else int(rng.integers(9, 50)) if i % 10 == 3 else 1, int(rng.integers(0, 300))) for i in range(60)]
     s = Step(reqs, 16, 8, 128, 16, seed=window, pad=4)
     s.check(max_q=70, mask=mask, window=window)
+
+
+# ------------------------------------------------------------------ scores that are NaN
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,old,max_q", [(1, 40, 1), (1, 5000, 1), (40, 30, 40), (40, 5000, 40), (3, 700, 0)])
+def test_a_nan_score_is_not_an_empty_row(n, old, max_q, d):
+    """lse = -inf says that a row saw no key. A row with a NaN among its scores, from its query or from a key, gets NaN in
+    o and lse, whole or joined from pieces; rows that do not see that key, and empty ones, keep their values."""
+    s = Step([(n, old), (n, 20)], 8, 2, d, 16, seed=n + old, pad=1)
+    s.kv[1] = n - 1                                   # its first row has position -1: no key
+    last = old + n - 1
+    s.q[0, 1, 5] = float("nan")                       # one head of one row
+    page, at = s.table[0, last // 16], last % 16
+    s.k[page, at, 1, 3] = float("nan")                # a key that only the last row sees, second key/value head
+    o, lse = s.run(max_q)
+    ref = s.oracle()
+    nan = np.isnan(ref["lse"])
+    assert nan.sum() == 1 + 4 and np.isneginf(ref["lse"][:, n]).all()
+    assert np.array_equal(np.isnan(lse.cpu().numpy()), nan)
+    rows = torch.tensor(nan.T, device="cuda")
+    assert torch.isnan(o[rows]).all()
+    o[rows], lse[torch.tensor(nan, device="cuda")] = 0.0, 0.0
+    ref = {**ref, **{x: np.where(nan, 0.0, ref[x]) for x in ("lse", "sqk")}, **{x: np.where(nan.T[..., None], 0.0, ref[x]) for x in ("o", "absv")}}
+    hold(o, lse, ref, d)
 
 
 # ------------------------------------------------------------------ graphs and whole steps

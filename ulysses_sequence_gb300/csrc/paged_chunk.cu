@@ -495,7 +495,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, units++ & 1, ab, ROLE_EPI, 1));
             if (!ok) break;
             tc_fence_after();
-            const bool any_key = l_sum > 0.f;
+            const bool any_key = l_sum != 0.f;  // NaN scores stay NaN
             const int slot = u.slot;
             const float inv = slot >= 0 ? 1.0f : (any_key ? 1.0f / l_sum : 0.f);
             const int unit_row = t * TOK * p.G + row;

@@ -410,11 +410,11 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const PagedParams p, con
             o.w += e * y[k].w;
         }
     }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;  // 0: no key; NaN scores stay NaN
     const int row = u.row0 + r / p.G, h = u.head * p.G + r % p.G;
     *reinterpret_cast<uint2*>(p.o + (int64_t(row) * p.H + h) * D + col) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (col == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (col == 0) p.lse[int64_t(h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Tensor map of a pool's keys or values, (64 elements, token, head, page, 64-element chunk), for copies

@@ -377,11 +377,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         *reinterpret_cast<float4*>(p.parts.o + row * D + c4 * 4) = acc;
                         if (c4 == 0) p.parts.ml[row] = make_float2(m, l);
                     } else {
-                        const float inv = l > 0.f ? 1.0f / l : 0.f;
+                        const float inv = l == 0.f ? 0.f : 1.0f / l;  // 0: no key; NaN scores stay NaN
                         const int row = t.row0 + r / p.G, h = t.head * p.G + r % p.G;
                         *reinterpret_cast<uint2*>(p.o + (int64_t(row) * p.H + h) * D + c4 * 4) =
                             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                        if (c4 == 0) p.lse[int64_t(h) * p.T + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        if (c4 == 0) p.lse[int64_t(h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                     }
                 }
                 // the next copy into this stage comes after these reads and writes of it
