@@ -1,0 +1,44 @@
+"""Reads the paged attention kernels for what no run may show, because it would take a wait that runs out with copies or
+products still on their way: every way out of a kernel waits for them first."""
+
+import os
+import re
+
+import pytest
+
+import ulysses_sequence_gb300 as U
+
+CSRC = os.path.join(os.path.dirname(U.__file__), "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def enclosing(text, at):
+    """The heads (what stands between the last ;, { or } and the brace) of the blocks around position `at`, and of a
+    statement's own condition, inside the kernel."""
+    start = text.index("__global__")
+    heads, last = [], start
+    for i in range(start, at):
+        if text[i] == "{":
+            heads.append(text[last:i])
+        elif text[i] == "}":
+            heads.pop()
+        if text[i] in "{};":
+            last = i + 1
+    return heads[1:] + [text[last:at]]
+
+
+@pytest.mark.parametrize("name,waits", [("paged_decode.cu", 1), ("paged_chunk.cu", 4)])
+def test_kernels_wait_for_what_is_on_its_way_whatever_a_role_has_seen(name, waits):
+    """A role that finished well does not know that another one has given up since: its copies (the producer) and
+    products (the issuer) may still be on their way. So the wait depends on no role's own success."""
+    text = source(name)
+    found = [m.start() for m in re.finditer(r"\b(?:mbar|ring)_drain\b", text)]
+    assert len(found) == waits
+    for at in found:
+        for head in enclosing(text, at):
+            conditional = re.search(r"\bok\b", head) or ("else" in head and "warp ==" not in head)
+            assert not conditional, head

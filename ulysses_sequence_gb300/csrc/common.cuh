@@ -101,12 +101,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Abort 
 }
 
 // A bounded wait that ignores the abort flag: used only to drain copies and MMAs already
-// in flight before a CTA leaves after an abort.
+// in flight before a CTA leaves, after an abort or whatever the other roles have seen.
 static __device__ __noinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(a, parity)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+    }
+}
+
+// Parity of the last phase that `fills` fills of a ring of `stages` barriers leave behind at one stage, or -1 where
+// none has reached it.
+__host__ __device__ constexpr int ring_last_parity(int fills, int stage, int stages) {
+    return fills > stage ? ((fills - 1 - stage) / stages) & 1 : -1;
+}
+static_assert(ring_last_parity(0, 0, 3) == -1 && ring_last_parity(1, 0, 3) == 0 && ring_last_parity(1, 1, 3) == -1 &&
+              ring_last_parity(3, 2, 3) == 0 && ring_last_parity(4, 0, 3) == 1 && ring_last_parity(6, 0, 3) == 1 &&
+              ring_last_parity(7, 0, 3) == 0 && ring_last_parity(7, 1, 3) == 1, "parities of a ring's last fills");
+
+// Waits, with the limit of mbar_drain, until all fills of a ring have landed.
+template <int STAGES>
+__device__ __forceinline__ void ring_drain(uint64_t* full, int fills) {
+    for (int st = 0; st < STAGES; ++st) {
+        const int parity = ring_last_parity(fills, st, STAGES);
+        if (parity >= 0) mbar_drain(full + st, uint32_t(parity));
     }
 }
 

@@ -263,18 +263,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (lane == 0) {
             p.parts.meta[cta] = meta;
-            if (!ok) {
-                // copies already in flight land before the CTA can exit
-                if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
-                for (int st = 0; st < NSK; ++st) {
-                    const int n = nk > st ? (nk - 1 - st) / NSK + 1 : 0;
-                    if (n > 0) mbar_drain(k_full + st, (n - 1) & 1);
-                }
-                for (int st = 0; st < NSV; ++st) {
-                    const int n = nv > st ? (nv - 1 - st) / NSV + 1 : 0;
-                    if (n > 0) mbar_drain(v_full + st, (n - 1) & 1);
-                }
-            }
+            // every copy lands before the CTA can exit, also where another role has given up since
+            ring_drain<1>(q_full, nq);
+            ring_drain<NSK>(k_full, nk);
+            ring_drain<NSV>(v_full, nv);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
@@ -356,10 +348,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     umma_commit_one(one, v_empty + sv);
                 }
             }
-            if (!ok) {
-                umma_commit_one(one, drain);
-                mbar_drain(drain, 0);
-            }
+            // every product is over before the tensor memory is freed, also where a softmax warp has given up since
+            umma_commit_one(one, drain);
+            mbar_drain(drain, 0);
         }
     } else {
         // ------------------------------------------------------------------ softmax (tile t)
@@ -535,6 +526,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             done_with_piece();
             tc_fence_before();
         }
+        tmem_wait_st();  // of a warp that has given up with weights on their way
     }
     tc_fence_before();
     __syncwarp();

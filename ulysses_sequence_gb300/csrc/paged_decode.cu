@@ -203,11 +203,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 tile_desc(issued % C::STAGES)->flags = TILE_END;
                 mbar_arrive(full + issued % C::STAGES);
             }
-        } else if (lane == 0) {
-            // copies already in flight land before the CTA can exit
-            for (int s = 0; s < C::STAGES; ++s)
-                if (issued > s) mbar_drain(full + s, ((issued - 1 - s) / C::STAGES) & 1);
+            ++issued;
         }
+        // every copy lands before the CTA can exit, also where a consumer has given up since
+        if (lane == 0) ring_drain<C::STAGES>(full, issued);
     } else {
         // ------------------------------------------------------------------ consumers
         const int cw = warp - 1;
