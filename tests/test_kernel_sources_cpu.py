@@ -42,3 +42,24 @@ def test_kernels_wait_for_what_is_on_its_way_whatever_a_role_has_seen(name, wait
         for head in enclosing(text, at):
             conditional = re.search(r"\bok\b", head) or ("else" in head and "warp ==" not in head)
             assert not conditional, head
+
+
+ALIGNED = r"\btmem_(?:ld|st|wait|alloc)\w*\("
+MEETS = re.compile(r"__syncwarp\(\)|__syncthreads\(\)|__all_sync\(|__any_sync\(|__ballot_sync\(")
+
+
+@pytest.mark.parametrize("name", ["paged_chunk.cu"])
+def test_warps_meet_before_instructions_for_whole_warps(name):
+    """tcgen05.ld, .st, .wait and .alloc are for whole converged warps. Where rows leave a loop's turn early, clear their own
+    values, or threads loop over their own requests, the warp meets again before the next of them."""
+    text = source(name)
+    turns = [m.start() for m in re.finditer(r"if \(!valid\) continue;", text)]
+    apart = [m.end() for m in re.finditer(r"if \(key0 \+ row >= kv\)|paged_costs<", text)]
+    assert turns
+    for at in turns:  # the next turn begins at the head of the loop
+        at = [m.end() for m in re.finditer(r"\bfor \([^{]*\{", text[:at])][-1]
+        before = text[at:at + re.search(ALIGNED, text[at:]).start()]
+        assert MEETS.search(before), before
+    for at in apart:
+        before = text[at:at + re.search(ALIGNED, text[at:]).start()]
+        assert MEETS.search(before), before

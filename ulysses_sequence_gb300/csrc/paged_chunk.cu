@@ -154,6 +154,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (p.B > kFewRequests)
         paged_share_block<kTile, kChunkUnitCost, kChunkThreads>(p, kChunkMinCost, reinterpret_cast<int64_t*>(smem + C::OFF_SH), w);
     else if (p.B > kLaneRequests) paged_costs<kTile, kChunkUnitCost, kChunkThreads>(p, costs);
+    __syncwarp();  // threads leave their requests' loops one by one; what follows is for whole warps
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -474,6 +475,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             for (int x = 0; x < 8; ++x) st_shared_v4(a + c * C::CHUNK_BYTES + x * 16, 0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();  // rows that cleared and rows that did not, together again
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -497,6 +499,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
                 float o[32];
+                __syncwarp();  // rows that stored and rows that did not, together again
                 tmem_ld32(tO + x * 32, o);
                 tmem_wait_ld();
                 if (!valid) continue;
