@@ -63,3 +63,27 @@ def test_warps_meet_before_instructions_for_whole_warps(name):
     for at in apart:
         before = text[at:at + re.search(ALIGNED, text[at:]).start()]
         assert MEETS.search(before), before
+
+
+@pytest.mark.parametrize("name", ["attn_fwd.cu", "attn_bwd.cu", "proj.cu"])
+def test_rows_that_store_meet_the_others_before_the_next_columns(name):
+    """Where only rows inside the tensor store, or leave the turn, the warp meets before the next columns are read."""
+    text = source(name)
+    loops = [m.end() for m in re.finditer(r"\bfor \([^{]*\{", text)]
+    seen = 0
+    for m in re.finditer(r"if \(!valid\) continue;|if \(valid\) \{|if \(row < p\.M\) \{", text):
+        for at in (a for a in loops if a < m.start()):
+            body = text[at:m.start()]
+            inside = body.count("{") >= body.count("}") and all(body[:i].count("{") >= body[:i].count("}") for i in range(len(body)))
+            load = re.search(ALIGNED, body)
+            if inside and load and "mbar_wait" not in body:  # the loop whose turn reads the columns and stores them
+                seen += 1
+                assert MEETS.search(body[:load.start()]), body[:load.end()]
+    assert seen
+
+
+def test_the_lane_that_issued_a_reduction_is_back_before_the_next_columns():
+    text = source("attn_bwd.cu")
+    at = text.index("if (dq_lanes) stage_add(v, acc);")
+    before = text[at:at + re.search(ALIGNED, text[at:]).start()]
+    assert MEETS.search(before), before

@@ -631,6 +631,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 float x[32];
+                __syncwarp();  // keys that stored and keys that did not, together again
                 if (n_it > 0) {
                     tmem_ld32(tmem + tcol + lane_off + c * 32, x);
                     tmem_wait_ld();
@@ -706,6 +707,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tmem_wait_ld();
             float* acc = p.dq_acc + dq_block<D>(p, b * p.H + h, qstep, 0, wq) * kDqBlockFloats;
             if (dq_lanes) stage_add(v, acc);
+            __syncwarp();  // with the lane that issued the reduction
             tmem_ld32(tmem + C::T_DP + lane_off + 64, v);
             tmem_ld32(tmem + C::T_DP + lane_off + 96, v + 32);
             tmem_wait_ld();

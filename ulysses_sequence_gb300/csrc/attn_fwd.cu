@@ -477,6 +477,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 float o[32];
+                __syncwarp();  // rows that stored and rows that did not, together again
                 if (list.n > 0) {
                     tmem_ld32(tO + lane_off + i * 32, o);
                     tmem_wait_ld();

@@ -207,6 +207,7 @@ proj_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 const int col = n0 + c;
                 if (col >= p.N) break;  // warp-uniform
                 float v[32];
+                __syncwarp();  // rows that stored and rows that did not, together again
                 tmem_ld32(acc + c, v);
                 tmem_wait_ld();
                 int o = 0;
