@@ -1,4 +1,4 @@
-"""Reads the paged attention kernels for what no run may show, because it would take a wait that runs out with copies or
+"""Reads the kernels for what no run may show, because it would take a wait that runs out with copies or
 products still on their way: every way out of a kernel waits for them first."""
 
 import os
@@ -31,7 +31,8 @@ def enclosing(text, at):
     return heads[1:] + [text[last:at]]
 
 
-@pytest.mark.parametrize("name,waits", [("paged_decode.cu", 1), ("paged_chunk.cu", 4)])
+@pytest.mark.parametrize("name,waits", [("paged_decode.cu", 1), ("paged_chunk.cu", 4), ("attn_fwd.cu", 4), ("attn_bwd.cu", 4),
+                                        ("proj.cu", 2)])
 def test_kernels_wait_for_what_is_on_its_way_whatever_a_role_has_seen(name, waits):
     """A role that finished well does not know that another one has given up since: its copies (the producer) and
     products (the issuer) may still be on their way. So the wait depends on no role's own success."""

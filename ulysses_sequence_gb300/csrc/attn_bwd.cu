@@ -423,13 +423,11 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 ++ndo;
             }
-            if (!ok && lane == 0) {
-                mbar_drain(kv_full, 0);
-                for (int qs = 0; qs < 2; ++qs) {
-                    const int cnt = nq > qs ? (nq - 1 - qs) / 2 + 1 : 0;
-                    if (cnt > 0) mbar_drain(q_full + qs, (cnt - 1) & 1);
-                }
-                if (ndo > 0) mbar_drain(do_full, (ndo - 1) & 1);
+            if (lane == 0) {
+                // every copy lands before the CTA can exit, also where another role has given up since
+                ring_drain<1>(kv_full, 1);
+                ring_drain<2>(q_full, nq);
+                ring_drain<1>(do_full, ndo);
             }
         }
     } else if (warp == 1) {
@@ -519,10 +517,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             if (ok) umma_commit(dkdv_done);
-            else {
-                umma_commit(drain);
-                mbar_drain(drain, 0);
-            }
+            // every product is over before the tensor memory is freed, also where another role has given up since
+            umma_commit(drain);
+            mbar_drain(drain, 0);
         }
     } else if (warp < 10) {
         // ------------------------------------------------------------------ softmax, dS

@@ -253,18 +253,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 load_tile<D, true>(sV + sv * C::TILE_BYTES, &tm_v, v_full + sv, p, kt * kTile, h, b);
                 ++nv;
             }
-            if (!ok) {
-                // let copies already in flight land before the CTA can exit
-                mbar_drain(q_full, 0);
-                for (int st = 0; st < NSK; ++st) {
-                    const int ck = nk > st ? (nk - 1 - st) / NSK + 1 : 0;  // K loads issued to stage st
-                    if (ck > 0) mbar_drain(k_full + st, (ck - 1) & 1);
-                }
-                for (int st = 0; st < NSV; ++st) {
-                    const int cv = nv > st ? (nv - 1 - st) / NSV + 1 : 0;
-                    if (cv > 0) mbar_drain(v_full + st, (cv - 1) & 1);
-                }
-            }
+            // every copy lands before the CTA can exit, also where another role has given up since
+            ring_drain<1>(q_full, any ? 1 : 0);
+            ring_drain<NSK>(k_full, nk);
+            ring_drain<NSV>(v_full, nv);
         }
       } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
@@ -339,10 +331,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 in1 = nin1;
             }
             if (ok) umma_commit(o_done);
-            else {
-                umma_commit(drain);
-                mbar_drain(drain, 0);
-            }
+            // every product is over before the tensor memory is freed, also where a softmax warp has given up since
+            umma_commit(drain);
+            mbar_drain(drain, 0);
         }
       }
     } else {

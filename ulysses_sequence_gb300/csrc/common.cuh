@@ -388,6 +388,12 @@ __device__ __forceinline__ void umma_pair_commit_both(uint64_t* bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
         ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
+// the same on the leader's barrier alone
+__device__ __forceinline__ void umma_pair_commit_leader(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(uint16_t(1)) : "memory");
+}
 // TMA load into this CTA's shared memory whose completion counts on a barrier given by its
 // shared::cluster address (the leader's)
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_cluster,

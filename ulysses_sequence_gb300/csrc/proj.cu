@@ -143,16 +143,9 @@ proj_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     }
                 }
             }
-            if (!ok) {
-                // wait (bounded) for this CTA's stages' last loads to land: the leader's barrier
-                // tracks them, so only the leader can; the peer waits on its empty barriers
-                if (rank == 0) {
-                    for (int s = 0; s < C::STAGES; ++s) {
-                        const int cnt = issued > s ? (issued - 1 - s) / C::STAGES + 1 : 0;
-                        if (cnt > 0) mbar_drain(full + s, (cnt - 1) & 1);
-                    }
-                }
-            }
+            // wait (bounded) for the stages' last loads to land, also where another role has given up since: the
+            // leader's barrier tracks both CTAs', so only the leader can
+            if (rank == 0) ring_drain<C::STAGES>(full, issued);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer (leader)
@@ -182,10 +175,9 @@ proj_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
                 if (ok) umma_pair_commit_both(acc_full + a);
             }
-            if (!ok) {
-                umma_pair_commit_both(drain);
-                mbar_drain(drain, 0);
-            }
+            // every product is over before the tensor memory is freed, also where an epilogue has given up since
+            umma_pair_commit_leader(drain);
+            mbar_drain(drain, 0);
         }
     } else {
         // ------------------------------------------------------------------ epilogue (both CTAs)
