@@ -70,6 +70,8 @@ struct ChunkCfg {
     static constexpr bool AHEAD = D == 64;
     static constexpr uint32_t COL_O = (AHEAD ? 3 : 2) * kTile, TMEM_COLS = 512;
     static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory");
+    // the issuer names columns from 0, constants of its instructions: true of an allocation of the whole tensor memory
+    static_assert(TMEM_COLS == 512, "the allocation starts at column 0");
     static_assert(NSK + (AHEAD ? 2 : 1) <= kInfoRing, "tile descriptions outlive their readers");
 };
 
