@@ -1,0 +1,50 @@
+"""More refusals of the torch helpers that need no GPU."""
+
+import types
+
+import pytest
+import torch
+
+import ulysses_sequence_gb300 as U
+
+I32, BF16 = torch.int32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from ulysses_sequence_gb300 import build
+    build.build()
+    return U.load()
+
+
+def sized(*shape, dtype=I32):
+    """A tensor of this size without memory."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+FAKE = types.SimpleNamespace(device=-1, H_kv=1, d=64, ref=None)  # of a cache, where tensors without memory are
+
+
+def test_helpers_refuse_tensors_past_32_bits():
+    """The library's counts are 32-bit: a tensor with more tokens, requests, pages or list entries is refused, not taken by the
+    low bits of its size (2^32 + 5 tokens would be five)."""
+    n, one, table = 2 ** 32 + 5, sized(1), sized(1, 4)
+    rows = sized(n, 1, 64, dtype=BF16)
+    with pytest.raises(ValueError, match="32 bits"):
+        U.kv_append(rows, rows, FAKE, sized(n))
+    with pytest.raises(ValueError, match="32 bits"):
+        U.paged_attn_fwd(rows, FAKE, sized(2), one, table)
+    q = sized(1, 1, 64, dtype=BF16)
+    with pytest.raises(ValueError, match="32 bits"):
+        U.paged_attn_fwd(q, FAKE, sized(2), one, sized(1, n))
+    with pytest.raises(ValueError, match="32 bits"):
+        U.paged_attn_fwd(q, FAKE, sized(n + 1), sized(n), sized(n, 0))
+    with pytest.raises(ValueError, match="32 bits"):
+        U.page_plan(one, one, one, one, sized(1, n), 16, 10, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        U.page_plan(sized(n), sized(n), one, one, sized(n, 0), 16, 10, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        U.page_plan(one, one, sized(n), one, table, 16, 10, 1)
+    for shape in ((n, 16, 1, 64), (1, 2 ** 32 + 16, 1, 64), (1, 16, n, 64), (1, 16, 1, 2 ** 32 + 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            U.PagedCache(sized(*shape, dtype=BF16), sized(*shape, dtype=BF16))

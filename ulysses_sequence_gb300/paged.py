@@ -85,6 +85,8 @@ class PagedCache:
             raise ValueError("PagedCache: k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
         if k.dtype != _BF16 or v.dtype != _BF16 or k.stride(3) != 1:
             raise ValueError("PagedCache: k and v must be bf16 with contiguous heads")
+        if max(k.shape) > _INT_MAX:
+            raise ValueError(f"PagedCache: sizes must fit 32 bits, got {tuple(k.shape)}")
         if not k.is_cuda or k.device != v.device:
             raise ValueError("PagedCache: k and v must be on one CUDA device")
         self.k, self.v, self.device = k, v, k.get_device()
@@ -109,9 +111,11 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     if not (0 <= T <= _INT_MAX and -1 <= num_pages <= _INT_MAX and -1 <= page_size <= _INT_MAX):
         raise ValueError(f"{where}: T, num_pages and page_size must fit 32 bits, got {T}, {num_pages}, {page_size}")
     B, width = block_table.shape
+    capacity = free_pages.numel()
+    if B > _INT_MAX or width > _INT_MAX or capacity > _INT_MAX:
+        raise ValueError(f"{where}: requests, pages of a request and free pages must fit 32 bits, got {B}, {width}, {capacity}")
     dev = block_table.get_device()
     table_stride = _table_stride(block_table, B, dev, where)
-    capacity = free_pages.numel()
     one, many = (B,), (B + 1,)
     if not (cached_lens.shape == one and cached_lens.dtype is _I32 and cached_lens.get_device() == dev
             and cached_lens.is_contiguous()):
@@ -154,6 +158,8 @@ def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
     """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
     fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
     where, dev, T = "kv_append", cache.device, k.shape[0]
+    if T > _INT_MAX:
+        raise ValueError(f"{where}: tokens must fit 32 bits, got {T}")
     k_stride = _row_stride(k, T, cache.H_kv, cache.d, dev, "k", where)
     v_stride = _row_stride(v, T, cache.H_kv, cache.d, dev, "v", where)
     if not (slot_map.shape == (T,) and slot_map.dtype is _I32 and slot_map.get_device() == dev
@@ -188,6 +194,8 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
         raise ValueError(f"{where}: q must be [T][H][d], got {tuple(q.shape)}")
     T, H, d = shape = q.shape
     B, width = block_table.shape
+    if T > _INT_MAX or B > _INT_MAX or width > _INT_MAX:
+        raise ValueError(f"{where}: rows, requests and pages of a request must fit 32 bits, got {T}, {B}, {width}")
     q_stride = _row_stride(q, T, H, cache.d, dev, "q", where)
     table_stride = _table_stride(block_table, B, dev, where)
     if not (cu_q.shape == (B + 1,) and cu_q.dtype is _I32 and cu_q.get_device() == dev and cu_q.is_contiguous()):
