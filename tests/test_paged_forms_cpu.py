@@ -48,3 +48,19 @@ def test_helpers_refuse_tensors_past_32_bits():
     for shape in ((n, 16, 1, 64), (1, 2 ** 32 + 16, 1, 64), (1, 16, n, 64), (1, 16, 1, 2 ** 32 + 64)):
         with pytest.raises(ValueError, match="32 bits"):
             U.PagedCache(sized(*shape, dtype=BF16), sized(*shape, dtype=BF16))
+
+
+def test_helpers_refuse_tensors_of_too_few_dimensions():
+    scalar, row = sized(dtype=BF16), sized(64, dtype=BF16)
+    for k in (scalar, row):
+        with pytest.raises(ValueError, match="k must be"):
+            U.kv_append(k, k, FAKE, sized(1))
+        with pytest.raises(ValueError, match="q must be"):
+            U.paged_attn_fwd(k, FAKE, sized(2), sized(1), sized(1, 4))
+        with pytest.raises(ValueError, match="q must be"):
+            U.paged_attn_workspace(k, FAKE)
+    for table in (sized(), sized(4), sized(1, 2, 3)):
+        with pytest.raises(ValueError, match="block_table must be"):
+            U.paged_attn_fwd(sized(1, 1, 64, dtype=BF16), FAKE, sized(2), sized(1), table)
+        with pytest.raises(ValueError, match="block_table must be"):
+            U.page_plan(sized(1), sized(1), sized(1), sized(1), table, 16, 10, 1)

@@ -54,6 +54,10 @@ def _new(shape, dtype, device: int, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _no_table(x, where: str):
+    raise ValueError(f"{where}: block_table must be int32 [B][max_pages], got {x.dtype} {tuple(x.shape)}")
+
+
 def _table_stride(x, B: int, device: int, where: str) -> int:
     """Row stride of an int32 block table [B][max_pages] with contiguous rows on this device."""
     if x.dtype is _I32 and x.dim() == 2 and x.shape[0] == B and x.get_device() == device:
@@ -110,7 +114,7 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     where = "page_plan"
     if not (0 <= T <= _INT_MAX and -1 <= num_pages <= _INT_MAX and -1 <= page_size <= _INT_MAX):
         raise ValueError(f"{where}: T, num_pages and page_size must fit 32 bits, got {T}, {num_pages}, {page_size}")
-    B, width = block_table.shape
+    B, width = block_table.shape if block_table.dim() == 2 else _no_table(block_table, where)
     capacity = free_pages.numel()
     if B > _INT_MAX or width > _INT_MAX or capacity > _INT_MAX:
         raise ValueError(f"{where}: requests, pages of a request and free pages must fit 32 bits, got {B}, {width}, {capacity}")
@@ -157,7 +161,8 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
 def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
     """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
     fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
-    where, dev, T = "kv_append", cache.device, k.shape[0]
+    where, dev = "kv_append", cache.device
+    T = k.shape[0] if k.dim() else 0
     if T > _INT_MAX:
         raise ValueError(f"{where}: tokens must fit 32 bits, got {T}")
     k_stride = _row_stride(k, T, cache.H_kv, cache.d, dev, "k", where)
@@ -176,6 +181,8 @@ def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
     step of a program. Calls that may overlap on the GPU need one each."""
     if not -1 <= max_q <= _INT_MAX:
         raise ValueError(f"paged_attn_workspace: max_q must fit 32 bits, got {max_q}")
+    if q.dim() != 3:
+        raise ValueError(f"paged_attn_workspace: q must be [T][H][d], got {tuple(q.shape)}")
     n = U.ulysses_paged_attn_workspace_size(q.shape[1], cache.H_kv, cache.d, max_q)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
@@ -193,7 +200,7 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
     if q.dim() != 3:
         raise ValueError(f"{where}: q must be [T][H][d], got {tuple(q.shape)}")
     T, H, d = shape = q.shape
-    B, width = block_table.shape
+    B, width = block_table.shape if block_table.dim() == 2 else _no_table(block_table, where)
     if T > _INT_MAX or B > _INT_MAX or width > _INT_MAX:
         raise ValueError(f"{where}: rows, requests and pages of a request must fit 32 bits, got {T}, {B}, {width}")
     q_stride = _row_stride(q, T, H, cache.d, dev, "q", where)
