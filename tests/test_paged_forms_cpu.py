@@ -1,5 +1,7 @@
 """More refusals of the torch helpers that need no GPU."""
 
+import subprocess
+import sys
 import types
 
 import pytest
@@ -64,3 +66,24 @@ def test_helpers_refuse_tensors_of_too_few_dimensions():
             U.paged_attn_fwd(sized(1, 1, 64, dtype=BF16), FAKE, sized(2), sized(1), table)
         with pytest.raises(ValueError, match="block_table must be"):
             U.page_plan(sized(1), sized(1), sized(1), sized(1), table, 16, 10, 1)
+
+
+_WITHOUT_PRIVATE_NAMES = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import ulysses_sequence_gb300 as U
+i = torch.zeros(1, dtype=torch.int32)
+try:
+    U.page_plan(i, i, i, i, torch.zeros(1, 4, dtype=torch.int32), 16, 4, 1)
+except ValueError as e:
+    assert "CUDA" in str(e)
+    print("refused")
+"""
+
+
+def test_helpers_need_no_private_names_of_torch():
+    """Where a build of torch does not have the two short cuts that the helpers take, its public calls do."""
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_PRIVATE_NAMES], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
