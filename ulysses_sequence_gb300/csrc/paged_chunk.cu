@@ -29,10 +29,11 @@
 // Values behind a request's last key may be anything: in the tile that holds the end, warps 2-5 clear
 // those rows of V in shared memory before the product reads them (0 x NaN is NaN).
 //
-// What bounds it (32/8 heads of 128, 8192 new tokens over 16384 keys: 1000 us, 1.65 PFLOP/s, 0.86 of the
-// measured bf16 rate): a step of 256 rows and 128 keys takes 2970 cycles, of which the issuer spends 2100 on its
-// 32 MMAs, the tensor core's own rate, and 630 waiting for weights: a tile's chain softmax (1530) -> PV, S (1050)
-// is longer than the other tile's products. Tried and slower: one tile with three S buffers (the key/value
+// What bounds it (32/8 heads of 128, 8192 new tokens over 16384 keys: 1050 to 1060 us, 1.56 PFLOP/s, 0.82 of the
+// measured bf16 rate; 1000 us on the card where the other figures of this paragraph were taken): a step of 256 rows
+// and 128 keys takes 2970 cycles, of which the issuer spends 2100 on its 32 MMAs, the tensor core's own rate, and 630
+// waiting for weights: a tile's chain softmax (1530) -> PV, S (1050) is longer than the other tile's products.
+// Tried and slower: one tile with three S buffers (the key/value
 // traffic doubles and the L2 bounds it: 1420 us); 64-key halves with two S buffers a tile (N = 64 products
 // cost nearly what N = 128 do: 1200 us); half a row to a thread with 16 softmax warps (1195 us); PV issued by
 // halves of P (no difference). d = 64, P in columns of its own so that both tiles' scores come a key tile
@@ -48,8 +49,13 @@ namespace {
 constexpr int kChunkThreads = 320;
 constexpr int kChunkRows = 2 * kTile;
 constexpr int kChunkMaxCtas = 160;   // one per SM: sizes the workspace
-constexpr int kChunkMinCost = 4;     // share below which another CTA costs more than it gives
-constexpr int kChunkUnitCost = 3;    // fixed cost of a unit, in key tiles
+// The smallest share of a CTA, in key tiles. Only calls that leave CTAs idle notice: one chunk of 40 tokens over 1000 keys
+// takes 22.1 us with 4, 27.4 us with 8 and 19.5 us with 2, two of 100 over 500 24.0, 23.3 and 21.5 us. 4 is from before
+// such calls were measured.
+constexpr int kChunkMinCost = 4;
+// The fixed cost of a unit, in key tiles, with 1, 2, 3, 4: 24 mixed requests 88.2, 76.9, 77.3, 77.8 us (heads of 64: 69.8,
+// 58.1, 54.8, 55.3 us), four chunks of 512 tokens 226, 217, 210, 208 us.
+constexpr int kChunkUnitCost = 3;
 constexpr int kInfoRing = 8;         // tiles that the producer may describe ahead (it leads by at most 7)
 
 template <int D>
@@ -427,8 +433,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const float alpha = need ? ex2(m_used - m_new) : 1.0f;  // ex2(-inf) = 0 for a first maximum
                 if (need) m_used = m_new;
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                // the weights, rounded to bf16 for the matrix product (their sum is not), over the scores' first
-                // 64 columns, all read by now
+                // the weights over the scores' first 64 columns, all read by now. The matrix product takes them in bf16, the
+                // type of the values, off by at most 2^-8 of a weight; their sum is taken of the weights before
+                // (errors against 64 bits: 1.2 to 1.4 times those of fp32 weights)
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
                 float2 rs4[4] = {};
 #pragma unroll

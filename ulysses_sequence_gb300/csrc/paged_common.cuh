@@ -258,7 +258,8 @@ __device__ __forceinline__ int64_t paged_cost(const PagedParams& p, int i) {
 
 // Where this CTA's share of the line begins, for batches of up to kFewRequests requests, in two steps with
 // the block's barrier between them: every thread puts down a request's cost, then one warp finds the
-// place. The code runs once a launch, so it is kept short: its instruction fetches are most of its time.
+// place. The code runs once a launch, so it is kept short: its instruction fetches are most of its time (200 decoding
+// requests with a window: 13.3 us, against 13.7 us by the whole block, which larger batches take).
 constexpr int kFewRequests = 256;
 template <int KT, int OVH, int NT>
 __device__ __forceinline__ void paged_costs(const PagedParams& p, int64_t* costs /* [kFewRequests] */) {
@@ -295,7 +296,7 @@ __device__ __forceinline__ bool paged_share_warp(const PagedParams& p, int min_c
 }
 
 // The same for up to 32 requests, one to a lane, by one warp alone, without the barrier and the second look at the
-// request (one request of 1500 keys: 8.3 us against 8.7 us).
+// request (one request of 1500 keys: 8.4 us against 8.7 us).
 constexpr int kLaneRequests = 32;
 template <int KT, int OVH>
 __device__ __forceinline__ bool paged_share_lanes(const PagedParams& p, int min_cost, PagedWalk<KT, OVH>& w) {

@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
 constexpr int kAppendThreads = 128, kAppendFew = 2, kAppendMany = 16;
 constexpr int64_t kAppendManyPieces = 48 * kAppendThreads * kAppendMany;  // from here on, by key rows' pieces
 
-// n / d for n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and m = floor(2^32 (2^s - d) / d) + 1, the
-// quotient is floor((floor(n m / 2^32) + n) / 2^s).
+// n / d for n < 2^31 by a multiplication, after Granlund and Montgomery ("Division by invariant integers using
+// multiplication", 1994): with 2^(s-1) < d <= 2^s and m = floor(2^32 (2^s - d) / d) + 1, the quotient is
+// floor((floor(n m / 2^32) + n) / 2^s).
 struct FastDiv {
     uint32_t d, m, s;
     explicit FastDiv(uint32_t div = 1) : d(div), m(0), s(0) {
