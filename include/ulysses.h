@@ -267,6 +267,57 @@ int ulysses_usp_attn_bwd(ulysses_shape_t shape, int P_ring, const ulysses_mask_t
                          void *stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Rotary positions of queries and keys, and the RMS norm of each of their heads: what stands
+ * between the QKV projection and the attention. With x one head of d_h elements at position p:
+ *   z = w * x / sqrt(mean(x^2) + eps)   (without weights z = x),
+ *   y = z with each pair (a, b) of its first `rot` elements turned by the angle theta = p * f_e:
+ *       (A (a cos theta - b sin theta), A (b cos theta + a sin theta)).
+ * Pair e is (z_e, z_{e + rot/2}), or (z_2e, z_{2e+1}) when interleaved; elements from rot on pass
+ * as they are. turns[rot/2] (device): f_e / (2 pi) in units of 2^-64 turns a token, modulo 2^64, so
+ * angles are exact to 2^-31 turns at every position below 2^31; a scaling for long contexts is a
+ * choice of f_e and A. rot: a multiple of 16, at most d_h (0: the norm alone). */
+typedef struct {
+    const uint64_t *turns;
+    int rot;
+    int interleaved;    /* 0: pairs (e, e + rot/2); else (2e, 2e+1) */
+    float amplitude;    /* A */
+} ulysses_rope_t;
+
+/* The rotation (and norm) over a sharded layout, as ulysses_attn_fwd takes it: q, q_out with H heads, k,
+ * k_out with H_kv (head-sharded: Hkvp) heads, bf16. Global token s has position pos0 + s. w_q, w_k
+ * [d_h]: the norms' weights, fp32 when w_fp32 is nonzero, else bf16; both or neither (then eps is
+ * not used). The norm and rotation are computed in fp32 and rounded once. q_out may be q and k_out may be k
+ * (in place).
+ * TOKEN_SHARDED needs L % P == 0, but not H % P == 0 (the shards of the Ulysses-ring hybrid).
+ * Supported: d_h in {64, 128}, fewer than 2^31 rows (B * L, head-sharded P * B * L). Tensors 16-byte aligned. */
+int ulysses_qk_rope_fwd(ulysses_shape_t shape, int io_layout, const ulysses_rope_t *rope, int64_t pos0, const void *q,
+                        const void *k, const void *w_q, const void *w_k, int w_fp32, float eps, void *q_out, void *k_out,
+                        void *stream);
+
+/* Its gradient: dq_out, dk_out are those of q_out, k_out; dq, dk (bf16) those of q, k. With weights, q and
+ * k are the forward's inputs (not needed without), and dw_q, dw_k [d_h] (fp32) are written: sums in fp32
+ * over all tokens and heads in an order of their own, the same from run to run on one GPU model. dq may be dq_out
+ * or q, dk may be dk_out or k. workspace (with weights): ulysses_qk_rope_bwd_workspace_size(shape) bytes,
+ * 16-byte aligned, contents need not be initialised; calls whose work overlaps need their own. With B == 0 or
+ * L == 0, dw_q and dw_k are set to zero. */
+size_t ulysses_qk_rope_bwd_workspace_size(ulysses_shape_t shape);
+int ulysses_qk_rope_bwd(ulysses_shape_t shape, int io_layout, const ulysses_rope_t *rope, int64_t pos0, const void *dq_out,
+                        const void *dk_out, const void *q, const void *k, const void *w_q, const void *w_k, int w_fp32,
+                        float eps, void *dq, void *dk, float *dw_q, float *dw_k, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* The forward over packed serving rows: q [T][H][d_h], k [T][H_kv][d_h], rows q_stride and k_stride elements apart
+ * (slices of a fused QKV product), q_out and k_out likewise with strides of their own; multiples of 8, at
+ * least a row; a stride is not used when T is 1. In place as above, with equal strides. Positions: positions[T] (int32, any
+ * value) when not NULL; else those of the paged attention, row t of request i at kv_lens[i] - cu_q[i+1] + t
+ * with cu_q[B + 1], kv_lens[B] as ulysses_page_plan writes them (B requests), and rows that
+ * belong to no request are left as they were in q_out and k_out. H and H_kv need not divide one another. */
+int ulysses_qk_rope_rows(int T, int H, int H_kv, int d_h, const ulysses_rope_t *rope, const void *q, int64_t q_stride,
+                         const void *k, int64_t k_stride, const int32_t *positions, int B, const int32_t *cu_q,
+                         const int32_t *kv_lens, const void *w_q, const void *w_k, int w_fp32, float eps, void *q_out,
+                         int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/* ---------------------------------------------------------------------------------------
  * Serving from a paged key/value cache. A trained block answers requests whose keys and
  * values live in pages of page_size tokens anywhere in a pool; a block table names each
  * request's pages in order. Three calls make one step: ulysses_page_plan turns request
@@ -353,6 +404,43 @@ int ulysses_paged_attn_fwd(const ulysses_kv_cache_t *cache, int B, int T, int H,
                            float softmax_scale, const void *q, int64_t q_stride, const int32_t *cu_q,
                            const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride, int max_pages,
                            void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* A cache of the same form held in 8 bits: k and v are e4m3 codes (strides in elements of one byte, positive multiples of
+ * 16, pointers 16-byte aligned; otherwise as above), and for each block of `block` consecutive
+ * tokens of a page and each head a scale, a power of two held as its exponent plus 127 in one byte (e8m0):
+ *   key = code * 2^(k_scale[page][token / block][h] - 127),  [num_pages][page_size / block][H_kv] contiguous,
+ * values with v_scale alike. block: a power of two from 16 to page_size. Scales lie in [10, 246]
+ * (2^-117 to 2^119): every key and value is then exact in bf16. Other bytes give undefined values. d_h: a
+ * multiple of 16. */
+typedef struct {
+    void *k;
+    void *v;
+    uint8_t *k_scale;
+    uint8_t *v_scale;
+    int num_pages, page_size, H_kv, d_h;
+    int64_t page_stride, token_stride, head_stride;
+    int block;
+} ulysses_kv_cache8_t;
+
+/* ulysses_kv_append into an 8-bit cache. With a block's largest magnitude among the new tokens of a head, amax, and
+ * need = the smallest whole n with amax <= 448 * 2^n, kept to [-117, 119]:
+ *   - a block whose first token (offset 0 of the block) is among the new ones gets the scale 2^need;
+ *   - any other block keeps the larger of its scale and 2^need; where that grows, the codes of all its
+ *     tokens are rounded again at the new scale (exactly, but for codes that become subnormal);
+ *   - code = x / scale to the nearest (ties to even); magnitudes past 448 * 2^119 and infinities become 448, NaN stays
+ *     NaN and does not count for amax.
+ * Tokens of one block must be consecutive rows of one call, as ulysses_page_plan places them: rows of one
+ * block that are separated by another block's give undefined codes and scales in it. Tokens whose slot lies outside the pool
+ * are skipped. d_h: 64 or 128. */
+int ulysses_kv_append8(const ulysses_kv_cache8_t *cache, int T, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const int32_t *slot_map, void *stream);
+
+/* ulysses_paged_attn_fwd over an 8-bit cache: the attention over the keys and values that the codes and scales stand
+ * for; q, o and lse as there. Same arguments, limits, workspace (its size too) and rules. */
+int ulysses_paged_attn8_fwd(const ulysses_kv_cache8_t *cache, int B, int T, int H, int max_q, int mask_kind, int window,
+                            float softmax_scale, const void *q, int64_t q_stride, const int32_t *cu_q,
+                            const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride, int max_pages,
+                            void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Host helper: the block-sparse pattern "sliding window plus strided global key tiles".
  * Query tile qt gets key tiles max(0, qt - window_before) .. min(n - 1, qt + window_after)

@@ -43,12 +43,18 @@ class KVCacheStruct(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class RopeStruct(ctypes.Structure):
+    """ulysses_rope_t."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float)]
+
+
 EXPORTS = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_kv_seq_to_head", "ulysses_kv_head_to_seq_sum",
            "ulysses_a2a_pack", "ulysses_a2a_unpack",
            "ulysses_qkv_proj", "ulysses_out_proj", "ulysses_usp_workspace_size", "ulysses_usp_attn_fwd",
            "ulysses_usp_attn_bwd", "ulysses_attn_fwd", "ulysses_attn_bwd_workspace_size",
            "ulysses_attn_bwd", "ulysses_attn_bwd_noalloc", "ulysses_bsmask_build_window_global",
            "ulysses_page_plan", "ulysses_kv_append", "ulysses_paged_attn_workspace_size", "ulysses_paged_attn_fwd",
+           "ulysses_qk_rope_fwd", "ulysses_qk_rope_bwd_workspace_size", "ulysses_qk_rope_bwd", "ulysses_qk_rope_rows",
            "ulysses_get_device_status", "ulysses_selftest_timeout", "ulysses_status_string", "ulysses_shutdown")
 BWD_NOALLOC_SCRATCH_BYTES = 96 * 1024 * 1024  # ULYSSES_BWD_NOALLOC_SCRATCH_BYTES
 
@@ -92,6 +98,12 @@ def load() -> ctypes.CDLL:
     lib.ulysses_paged_attn_workspace_size.argtypes = [i, i, i, i]
     lib.ulysses_paged_attn_workspace_size.restype = sz
     lib.ulysses_paged_attn_fwd.argtypes = [cp, i, i, i, i, i, i, f, vp, i64, vp, vp, vp, i64, i, vp, vp, vp, sz, vp]
+    rp = ctypes.POINTER(RopeStruct)
+    lib.ulysses_qk_rope_fwd.argtypes = [Shape, i, rp, i64, vp, vp, vp, vp, i, f, vp, vp, vp]
+    lib.ulysses_qk_rope_bwd_workspace_size.argtypes = [Shape]
+    lib.ulysses_qk_rope_bwd_workspace_size.restype = sz
+    lib.ulysses_qk_rope_bwd.argtypes = [Shape, i, rp, i64, vp, vp, vp, vp, vp, vp, i, f, vp, vp, vp, vp, vp, sz, vp]
+    lib.ulysses_qk_rope_rows.argtypes = [i, i, i, i, rp, vp, i64, vp, i64, vp, i, vp, vp, vp, vp, i, f, vp, i64, vp, i64, vp]
     lib.ulysses_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.ulysses_selftest_timeout.argtypes = [vp]
     lib.ulysses_status_string.argtypes = [i]
@@ -99,7 +111,7 @@ def load() -> ctypes.CDLL:
     lib.ulysses_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
         if name not in ("ulysses_attn_bwd_workspace_size", "ulysses_usp_workspace_size",
-                        "ulysses_paged_attn_workspace_size", "ulysses_status_string"):
+                        "ulysses_paged_attn_workspace_size", "ulysses_qk_rope_bwd_workspace_size", "ulysses_status_string"):
             getattr(lib, name).restype = i
     _lib = lib
     return lib
@@ -228,6 +240,29 @@ def ulysses_paged_attn_fwd(cache: Optional[KVCacheStruct], B: int, T: int, H: in
     return load().ulysses_paged_attn_fwd(_mref(cache), B, T, H, max_q, mask_kind, window, softmax_scale, q, q_stride,
                                          cu_q, kv_lens, block_table, table_stride, max_pages, o, lse, workspace,
                                          workspace_bytes, stream)
+
+
+def ulysses_qk_rope_fwd(shape: Shape, io_layout: int, rope: Optional[RopeStruct], pos0: int, q: int, k: int, w_q: int, w_k: int,
+                        w_fp32: int, eps: float, q_out: int, k_out: int, stream: int) -> int:
+    return load().ulysses_qk_rope_fwd(shape, io_layout, _mref(rope), pos0, q, k, w_q, w_k, w_fp32, eps, q_out, k_out, stream)
+
+
+def ulysses_qk_rope_bwd_workspace_size(shape: Shape) -> int:
+    return load().ulysses_qk_rope_bwd_workspace_size(shape)
+
+
+def ulysses_qk_rope_bwd(shape: Shape, io_layout: int, rope: Optional[RopeStruct], pos0: int, dq_out: int, dk_out: int, q: int, k: int,
+                        w_q: int, w_k: int, w_fp32: int, eps: float, dq: int, dk: int, dw_q: int, dw_k: int, workspace: int,
+                        workspace_bytes: int, stream: int) -> int:
+    return load().ulysses_qk_rope_bwd(shape, io_layout, _mref(rope), pos0, dq_out, dk_out, q, k, w_q, w_k, w_fp32, eps, dq, dk, dw_q,
+                                      dw_k, workspace, workspace_bytes, stream)
+
+
+def ulysses_qk_rope_rows(T: int, H: int, H_kv: int, d_h: int, rope: Optional[RopeStruct], q: int, q_stride: int, k: int, k_stride: int,
+                         positions: int, B: int, cu_q: int, kv_lens: int, w_q: int, w_k: int, w_fp32: int, eps: float, q_out: int,
+                         q_out_stride: int, k_out: int, k_out_stride: int, stream: int) -> int:
+    return load().ulysses_qk_rope_rows(T, H, H_kv, d_h, _mref(rope), q, q_stride, k, k_stride, positions, B, cu_q, kv_lens, w_q, w_k,
+                                       w_fp32, eps, q_out, q_out_stride, k_out, k_out_stride, stream)
 
 
 def ulysses_get_device_status(stream: int) -> Tuple[int, int]:
@@ -506,10 +541,18 @@ def attn_bwd(q, k, v, o, lse, do, P: int, mask: Mask, layout: int = LAYOUT_TOKEN
 _PAGED = ("PagedCache", "page_plan", "kv_append", "paged_attn_workspace", "paged_attn_fwd")
 
 
+# Those of the rotary calls are in rope.py.
+_ROPE = ("Rope", "rope_frequencies", "qk_rope_fwd", "qk_rope_bwd", "qk_rope_rows")
+
+
 def __getattr__(name: str):
     if name in _PAGED:
         from . import paged
         globals().update((n, getattr(paged, n)) for n in _PAGED)
+        return globals()[name]
+    if name in _ROPE:
+        from . import rope
+        globals().update((n, getattr(rope, n)) for n in _ROPE)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

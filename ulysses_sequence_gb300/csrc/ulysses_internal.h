@@ -111,6 +111,32 @@ int launch_usp_bwd(const ulysses_shape_t& s, int P_ring, const MaskArgs& m, floa
 int launch_proj_gemm(int M, int N, int K, const void* a, const void* b, int n_out, const int* col0, void* const* out,
                      const int* ld, cudaStream_t stream);
 
+// ---- rotary positions and head norms (rope.cu), one validated call
+struct RopeTensors {  // q or k
+    const void *x, *dy;             // forward: input; backward: the forward's input and the gradient of its output
+    void* out;
+    const void* w;                  // nullptr: no norm
+    float* dw;
+    int64_t x_stride, out_stride;   // elements between rows (dy as x)
+    int heads;
+};
+struct RopeArgs {
+    RopeTensors q, k;
+    ulysses_rope_t rope;
+    bool back, wide;                // wide: weights are fp32
+    float eps;
+    int d, rows;
+    // positions of the rows: given; or of requests; or pos0 + m % seg + m / shard_rows * shard_step
+    const int32_t *positions, *cu_q, *kv_lens;
+    int B;
+    int64_t pos0;
+    int seg, shard_rows;
+    int64_t shard_step;
+    void* workspace;
+};
+int launch_rope(const RopeArgs& a, cudaStream_t stream);
+size_t rope_bwd_workspace_bytes(int H, int Hkv, int d);  // heads of a row
+
 // ---- serving from a paged key/value cache
 constexpr int kPlanMaxB = 8192;       // requests of one page plan (its prefix sums live in shared memory)
 constexpr int kPagedMaxLen = 1 << 30; // keys of a request, rows of a call: sums of two fit an int32
