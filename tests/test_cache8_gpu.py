@@ -1,0 +1,307 @@
+"""GPU parity of the 8-bit cache against its oracle. Codes and scales must be equal. Attention is held to the bounds of
+test_paged_gpu.py, of the keys and values that codes and scales stand for (all of them exact in bf16): the kernels' weights
+are rounded to 11 bits or to 8, their queries at most to what is 2^-28 of a row's largest."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache8 as cache8
+import oracle.paged as paged
+import ulysses_sequence_gb300 as U
+from gpu_util import need_gpu
+from test_paged_gpu import KV, Step, healthy, hold, i32
+
+pytestmark = pytest.mark.gpu
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def raw(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+def device(x, dtype, head_major=False):
+    """A uint8 array on the GPU as dtype; [page][token][head][d] in head-major memory where asked."""
+    t = torch.tensor(x, device="cuda")
+    return (t.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3) if head_major else t).view(dtype)
+
+
+# ------------------------------------------------------------------ append
+
+def bf16_rows(rng, *shape, spread=4.0):
+    """Rows whose heads differ in size by up to 2^spread either way."""
+    x = rng.standard_normal(shape) * 2.0 ** rng.uniform(-spread, spread, (*shape[:-1], 1))
+    return torch.tensor(x, dtype=torch.float32).to(torch.bfloat16)
+
+
+def run_append(codes, scales, rows, slots, block, head_major=False, fused=False):
+    """codes, scales, rows: pairs (keys, values). Checks the GPU against the oracle and returns what it left."""
+    kc, vc = (device(c, E4M3, head_major) for c in codes)
+    ks, vs = (device(s, E8M0) for s in scales)
+    x = [r.cuda() for r in rows]
+    if fused:
+        both = torch.cat([torch.zeros_like(x[0]), x[0], x[1]], 1)
+        H = x[0].shape[1]
+        x = [both[:, H:2 * H], both[:, 2 * H:]]
+    U.kv_append(x[0], x[1], U.PagedCache8(kc, vc, ks, vs), i32(slots))
+    healthy()
+    got = []
+    for c, s, r, gc, gs in zip(codes, scales, rows, (kc, vc), (ks, vs)):
+        wc, ws = cache8.append(c, s, r.double().numpy(), slots, block)
+        assert np.array_equal(raw(gs), ws), np.argwhere(raw(gs) != ws)[:4]
+        assert np.array_equal(raw(gc), wc), np.argwhere(raw(gc) != wc)[:4]
+        got.append((wc, ws))
+    return got
+
+
+def pool(rng, pages, page, H, d, block):
+    """Random codes (all patterns, NaN too) and scales around 1, of keys and of values."""
+    return ([rng.integers(0, 256, (pages, page, H, d)).astype(np.uint8) for _ in range(2)],
+            [rng.integers(110, 130, (pages, page // block, H)).astype(np.uint8) for _ in range(2)])
+
+
+def placed(rng, lens, page, pages):
+    """Slots of requests (first offset, tokens), each from that offset of a page of its own on, pages anywhere."""
+    order, slots = list(rng.permutation(pages)), []
+    for off, n in lens:
+        for t in range(off, off + n):
+            if t == off or t % page == 0:
+                p = order.pop()
+            slots.append(p * page + t % page)
+    return np.array(slots)
+
+
+@pytest.mark.parametrize("H,d,page,block,head_major,fused", [(8, 128, 64, 64, False, False), (1, 64, 16, 16, False, True),
+                                                             (5, 128, 256, 32, True, False), (3, 64, 128, 128, False, True),
+                                                             (20, 64, 64, 16, True, False), (2, 128, 4096, 4096, False, False)])
+def test_append_matches_oracle(H, d, page, block, head_major, fused):
+    """Single tokens in the middle, at the start and at the end of blocks, chunks that begin anywhere and pass block and page ends,
+    rows of no slot among them."""
+    rng = np.random.default_rng(H * d + block)
+    lens = [(0, 1), (block - 1, 1), (3, 1), (page - 1, 2), (7, 2 * block + 5), (0, page + 1), (block // 2, 16), (1, 17), (block - 1, 33), (0, 0)]
+    pages = sum((o + n - 1) // page + 1 for o, n in lens) + 2
+    slots = placed(rng, lens, page, pages)
+    pad = [-1, pages * page, 2 ** 31 - 1, -2 ** 31]
+    slots = np.concatenate([pad[:1], slots[:3], pad[1:2], slots[3:], pad[2:]])
+    codes, scales = pool(rng, pages, page, H, d, block)
+    rows = [bf16_rows(rng, len(slots), H, d) for _ in range(2)]
+    codes, scales = zip(*run_append(codes, scales, rows, slots, block, head_major, fused))
+    # the next tokens of the same blocks: scales grow or stay
+    later = [s + 1 if 0 <= s < pages * page and (s + 1) % block else -1 for s in slots]
+    keep = [i for i, s in enumerate(later) if s not in slots or s < 0]
+    rows = [bf16_rows(rng, len(keep), H, d) for _ in range(2)]
+    run_append(codes, scales, rows, np.array(later)[keep], block, head_major, fused)
+
+
+@pytest.mark.parametrize("T", [64, 700, 3000, 9001])
+def test_append_windows(T):
+    """Enough rows for every window that a block of threads looks through; single tokens and a prompt."""
+    rng = np.random.default_rng(T)
+    H, d, page, block = 8, 64, 32, 16
+    pages = T + 3
+    codes, scales = pool(rng, pages, page, H, d, block)
+    singles = rng.permutation(pages)[:T] * page + rng.integers(0, page, T)
+    rows = [bf16_rows(rng, T, H, d) for _ in range(2)]
+    run_append(codes, scales, rows, singles, block)
+    run_append(codes, scales, rows, placed(rng, [(5, T)], page, pages), block)
+
+
+def test_append_of_extreme_values():
+    """Zeros, the smallest and the largest bf16, infinities and NaN; magnitudes at and next to 448 * 2^n."""
+    d = 64
+    x = torch.zeros(12, 1, d)
+    x[1, 0, 3] = 2.0 ** -133
+    x[2, 0, :] = torch.finfo(torch.bfloat16).max
+    x[3, 0, 5], x[3, 0, 6] = float("inf"), -float("inf")
+    x[4, 0, 7], x[4, 0, 8] = float("nan"), 3.0
+    x[5, 0, :] = float("nan")
+    x[6, 0, 0], x[7, 0, 0], x[8, 0, 0] = 448.0, 450.0, 446.0
+    x[9, 0, 0], x[10, 0, 0], x[11, 0, 0] = 448.0 * 2.0 ** -117, 2.0 ** -126, -0.0
+    x = x.to(torch.bfloat16)
+    for offset in (0, 5):  # blocks begun by these rows, and blocks with tokens of the smallest scale
+        codes = [np.full((12, 16, 1, d), 0x38, np.uint8) for _ in range(2)]
+        scales = [np.full((12, 1, 1), 10 if offset else 200, np.uint8) for _ in range(2)]
+        run_append(codes, scales, [x, x], np.arange(12) * 16 + offset, 16)
+
+
+def test_growing_scales_round_older_tokens_again():
+    """Every code, at shifts up to past its last bit: the same as rounding the value at the new scale."""
+    for shift in (1, 2, 5, 9, 16, 25, 60, 200):
+        codes = [np.arange(256, dtype=np.uint8).reshape(1, 16, 1, 16).repeat(4, 3) for _ in range(2)]
+        scales = [np.full((1, 1, 1), 30, np.uint8) for _ in range(2)]
+        x = torch.zeros(1, 1, 64)
+        x[0, 0, 0] = 448.0 * 2.0 ** (30 + shift - 127)
+        run_append(codes, scales, [x.to(torch.bfloat16)] * 2, np.array([3]), 16)
+
+
+def test_append_offsets_past_32_bits():
+    pages, page, H, d = 2200, 4096, 4, 128
+    kc, vc = (torch.zeros((pages, page, H, d), dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2))
+    assert kc.numel() > 2 ** 32
+    ks, vs = (torch.full((pages, 256, H), 127, dtype=torch.uint8, device="cuda").view(E8M0) for _ in range(2))
+    k, v = torch.randn(2, 3, H, d, device="cuda").to(torch.bfloat16)
+    slots = [pages * page - 1, pages * page - 4096, 17]
+    U.kv_append(k, v, U.PagedCache8(kc, vc, ks, vs), i32(slots))
+    for c, s, x in ((kc, ks, k), (vc, vs, v)):
+        c, s = c.view(torch.uint8).view(-1, H, d), s.view(torch.uint8).view(-1, H)
+        for t, at in enumerate(slots):
+            fresh = at % 16 == 0
+            wc, ws = cache8.append(np.zeros((1, 16, H, d), np.uint8), np.full((1, 1, H), 127, np.uint8), x[t:t + 1].double().cpu().numpy(),
+                                   np.array([at % 16]), 16)
+            assert np.array_equal(raw(c[at]), wc[0, at % 16]) and np.array_equal(raw(s[at // 16]), ws[0, 0]), fresh
+        assert int(torch.count_nonzero((c & 127).amax((1, 2)))) == 3
+
+
+# ------------------------------------------------------------------ attention
+
+class Step8(Step):
+    """A step whose pools are rounded to 8 bits, block by block, after the blocks have been given sizes of their own: 2^k within
+    `k_spread` for keys (they move scores), v_spread for values. self.k and self.v then hold what codes and scales stand for."""
+
+    def __init__(self, reqs, H, Hkv, d, page, block=16, k_spread=1, v_spread=6, head_major=False, seed=0, **kw):
+        super().__init__(reqs, H, Hkv, d, page, head_major=head_major, seed=seed, **kw)
+        rng = np.random.default_rng(seed + 1)
+        pages = self.k.shape[0]
+        parts = []
+        for name, spread in (("k", k_spread), ("v", v_spread)):
+            x = getattr(self, name).float().cpu().numpy().astype(np.float64).reshape(pages, page // block, block, Hkv, d)
+            x = x * 2.0 ** rng.integers(-spread, spread + 1, (pages, page // block, 1, Hkv, 1))
+            top = np.nanmax(np.where(np.isnan(x), 0, np.abs(x)), axis=(2, 4))
+            n = np.vectorize(cache8.need)(top)
+            scale = np.where(top > 0, n + 127, rng.integers(10, 247, n.shape)).astype(np.uint8)
+            codes = cache8.encode(x * 2.0 ** (127.0 - scale[:, :, None, :, None])).reshape(pages, page, Hkv, d)
+            parts.append((codes, scale))
+        self.block, self.parts = block, parts
+        self.put(head_major)
+
+    def put(self, head_major=False):
+        (kc, ks), (vc, vs) = self.parts
+        self.cache = U.PagedCache8(device(kc, E4M3, head_major), device(vc, E4M3, head_major), device(ks, E8M0), device(vs, E8M0))
+        self.k, self.v = (torch.tensor(cache8.values(c, s, self.block)) for c, s in self.parts)
+
+
+@pytest.mark.parametrize("H,Hkv,d,page,block,head_major", [(8, 2, 128, 16, 16, False), (4, 4, 64, 32, 16, True), (16, 1, 128, 64, 64, False),
+                                                           (6, 2, 64, 128, 32, False), (5, 1, 128, 256, 128, True), (1, 1, 64, 16, 16, False)])
+def test_decode_lengths(H, Hkv, d, page, block, head_major):
+    s = Step8([(1, c) for c in KV], H, Hkv, d, page, block, seed=H + d, head_major=head_major, pad=3, q_extra=2)
+    s.check(max_q=1)
+    s.check(max_q=0)
+    healthy()
+
+
+@pytest.mark.parametrize("mask,window", [("causal", 0), ("none", 0), ("causal", 1), ("causal", 37), ("causal", 128), ("causal", 700)])
+@pytest.mark.parametrize("d,G,n,page,block", [(128, 4, 1, 16, 16), (64, 4, 4, 16, 16), (128, 5, 3, 64, 32), (64, 1, 1, 128, 128),
+                                              (128, 1, 16, 32, 16), (64, 5, 2, 512, 256)])
+def test_masks_in_the_decode_kernel(mask, window, d, G, n, page, block):
+    old = (0, 3, 15, 16, 62, 63, 64, 127, 128, 129, 255, 256, 800)   # around the ends of pages and tiles, past each window
+    reqs = [(0 if i == 4 else max(1, n - i % 2), c) for i, c in enumerate(old)]
+    s = Step8(reqs, 2 * G, 2, d, page, block, seed=window + n, pad=3)
+    s.check(max_q=n, mask=mask, window=window)
+    if window > 0:
+        for i, (_, c) in enumerate(reqs):
+            s.table[i, :max(0, c - window + 1) // page] = -1
+        s.check(max_q=n, mask=mask, window=window)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 16, 17, 31, 33, 64, 65, 130])
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (3, 3, 64), (7, 1, 128)])
+def test_few_and_chunk_lengths(n, H, Hkv, d):
+    s = Step8([(n, c) for c in (0, 1, 30, 127, 128, 200)], H, Hkv, d, 16, seed=n, pad=1)
+    s.check(max_q=n)
+
+
+@pytest.mark.parametrize("n", [1, 5, 100])
+def test_long_contexts_split_over_the_grid(n):
+    Step8([(n, 5000), (1, 3)], 8, 1, 128, 64, 64, seed=n).check(max_q=n)
+
+
+def test_rows_that_see_nothing_and_missing_pages():
+    for max_q, H, Hkv in ((1, 4, 2), (20, 4, 2), (0, 8, 1)):
+        n = max_q or 40
+        s = Step8([(n, 5), (n, 0), (n, 200), (n, 300), (n, 90)], H, Hkv, 128, 16, seed=n)
+        s.kv = [max(0, n // 2), 0, 200 + n, 300 + n, 90 + n]
+        s.table[3, 0], s.table[3, 5], s.table[3, -1] = -1, s.cache.num_pages, 10 ** 9
+        s.table[4, :] = -1
+        s.check(max_q=max_q)
+        assert np.isneginf(s.oracle()["lse"]).any()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_very_different_scales(n, d):
+    """Value scales 2^30 apart from block to block, and blocks whose size the softmax all but hides: each row is held to its own
+    terms."""
+    s = Step8([(n, 700), (n, 90)], 8, 2, d, 32, 16, v_spread=30, seed=n + d)
+    s.check(max_q=n)
+    s = Step8([(n, 700), (n, 90)], 8, 2, d, 32, 16, v_spread=30, k_spread=3, q_scale=4.0, seed=n + d)
+    s.check(max_q=n)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("shift", [-100, -30, 0, 60])
+def test_scales_at_the_ends(n, shift):
+    """Queries 2^-shift, keys 2^shift, values at the smallest scales or near the largest."""
+    s = Step8([(n, 300)], 4, 2, 64, 16, seed=n)
+    (kc, ks), (vc, vs) = s.parts
+    ks = (ks.astype(int) + shift).clip(10, 246).astype(np.uint8)
+    vs = np.where(np.arange(vs.size).reshape(vs.shape) % 2 == 0, 10 if shift < 0 else 235, vs).astype(np.uint8)
+    s.parts = [(kc, ks), (vc, vs)]
+    s.q = (s.q.double() * 2.0 ** -shift).to(torch.bfloat16)
+    s.put()
+    s.check(max_q=n)
+
+
+def test_queries_of_very_different_elements():
+    """Elements of a row down to 2^-24 of its largest, and rows of zeros."""
+    s = Step8([(1, 200), (3, 90), (40, 100)], 8, 2, 128, 16, seed=5)
+    x = s.q.float() * torch.exp2(torch.randint(-24, 1, s.q.shape, device="cuda").float())
+    x[::5] = 0
+    s.q = x.to(torch.bfloat16)
+    s.check(max_q=40)
+
+
+def test_same_bits_every_time():
+    s = Step8([(1, c) for c in (3000, 10, 700)], 8, 2, 128, 16, seed=1)
+    a, b = s.run(1), s.run(1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------------ as they are used
+
+def test_serving_steps_with_norms_and_rotation():
+    """plan -> norm and rotation -> append -> attention, in chunks and single tokens, against the oracles' chain on the codes that
+    the cache holds, the appended codes against the oracle's from the rotated rows."""
+    H, Hkv, d, page, block, B = 8, 2, 128, 32, 16, 3
+    rng = np.random.default_rng(7)
+    num, width = 60, 16
+    cache = U.PagedCache8.empty(num, page, Hkv, d, block)
+    cache.k.view(torch.uint8).fill_(0x7f)
+    cache.v.view(torch.uint8).fill_(0x7f)
+    rope = U.Rope(d)
+    w = [torch.tensor(1 + 0.1 * rng.standard_normal(d), dtype=torch.float32, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    table = i32(np.full((B, width), -1))
+    free, n_free, cached = i32(rng.permutation(num)), i32([num]), i32([0] * B)
+    codes = [raw(cache.k), raw(cache.v)]
+    scales = [raw(cache.k_scale), raw(cache.v_scale)]
+    for step, new in enumerate(([40, 0, 7], [1, 100, 1], [1, 1, 1], [1, 1, 0], [30, 1, 1], [1, 1, 1])):
+        T = sum(new) + 2
+        rows = bf16_rows(rng, T, H + 2 * Hkv, d, spread=1.0).cuda()
+        q, k, v = rows[:, :H], rows[:, H:H + Hkv], rows[:, H + Hkv:]
+        cu, kv, slots, info = U.page_plan(cached, i32(new), free, n_free, table, page, num, T)
+        U.qk_rope_rows(q, k, rope, cu_q=cu, kv_lens=kv, w_q=w[0], w_k=w[1], q_out=q, k_out=k)
+        U.kv_append(k, v, cache, slots)
+        o, lse = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((H, T), 7.0, device="cuda")
+        U.paged_attn_fwd(q, cache, cu, kv, table, max(new), o=o, lse=lse)
+        cached, n_free = kv, n_free - info[1:2]
+        for i, (x, c, s) in enumerate(((k, cache.k, cache.k_scale), (v, cache.v, cache.v_scale))):
+            codes[i], scales[i] = cache8.append(codes[i], scales[i], x.double().cpu().numpy(), slots.cpu().numpy(), block)
+            assert np.array_equal(raw(c), codes[i]) and np.array_equal(raw(s), scales[i]), step
+        pools = [cache8.values(c, s, block) for c, s in zip(codes, scales)]
+        ref = paged.paged_attention(q.double().cpu().numpy(), *pools, cu.cpu().numpy(), kv.cpu().numpy(), table.cpu().numpy(), True)
+        hold(o, lse, ref, d)

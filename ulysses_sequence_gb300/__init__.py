@@ -43,6 +43,14 @@ class KVCacheStruct(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class KVCache8Struct(ctypes.Structure):
+    """ulysses_kv_cache8_t; strides in elements of one byte."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("H_kv", ctypes.c_int), ("d_h", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("block", ctypes.c_int)]
+
+
 class RopeStruct(ctypes.Structure):
     """ulysses_rope_t."""
     _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float)]
@@ -54,6 +62,7 @@ EXPORTS = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_kv_seq_to_head
            "ulysses_usp_attn_bwd", "ulysses_attn_fwd", "ulysses_attn_bwd_workspace_size",
            "ulysses_attn_bwd", "ulysses_attn_bwd_noalloc", "ulysses_bsmask_build_window_global",
            "ulysses_page_plan", "ulysses_kv_append", "ulysses_paged_attn_workspace_size", "ulysses_paged_attn_fwd",
+           "ulysses_kv_append8", "ulysses_paged_attn8_fwd",
            "ulysses_qk_rope_fwd", "ulysses_qk_rope_bwd_workspace_size", "ulysses_qk_rope_bwd", "ulysses_qk_rope_rows",
            "ulysses_get_device_status", "ulysses_selftest_timeout", "ulysses_status_string", "ulysses_shutdown")
 BWD_NOALLOC_SCRATCH_BYTES = 96 * 1024 * 1024  # ULYSSES_BWD_NOALLOC_SCRATCH_BYTES
@@ -98,6 +107,9 @@ def load() -> ctypes.CDLL:
     lib.ulysses_paged_attn_workspace_size.argtypes = [i, i, i, i]
     lib.ulysses_paged_attn_workspace_size.restype = sz
     lib.ulysses_paged_attn_fwd.argtypes = [cp, i, i, i, i, i, i, f, vp, i64, vp, vp, vp, i64, i, vp, vp, vp, sz, vp]
+    c8 = ctypes.POINTER(KVCache8Struct)
+    lib.ulysses_kv_append8.argtypes = [c8, i, vp, i64, vp, i64, vp, vp]
+    lib.ulysses_paged_attn8_fwd.argtypes = [c8, i, i, i, i, i, i, f, vp, i64, vp, vp, vp, i64, i, vp, vp, vp, sz, vp]
     rp = ctypes.POINTER(RopeStruct)
     lib.ulysses_qk_rope_fwd.argtypes = [Shape, i, rp, i64, vp, vp, vp, vp, i, f, vp, vp, vp]
     lib.ulysses_qk_rope_bwd_workspace_size.argtypes = [Shape]
@@ -240,6 +252,20 @@ def ulysses_paged_attn_fwd(cache: Optional[KVCacheStruct], B: int, T: int, H: in
     return load().ulysses_paged_attn_fwd(_mref(cache), B, T, H, max_q, mask_kind, window, softmax_scale, q, q_stride,
                                          cu_q, kv_lens, block_table, table_stride, max_pages, o, lse, workspace,
                                          workspace_bytes, stream)
+
+
+def ulysses_kv_append8(cache: Optional[KVCache8Struct], T: int, k: int, k_stride: int, v: int, v_stride: int,
+                       slot_map: int, stream: int) -> int:
+    return load().ulysses_kv_append8(_mref(cache), T, k, k_stride, v, v_stride, slot_map, stream)
+
+
+def ulysses_paged_attn8_fwd(cache: Optional[KVCache8Struct], B: int, T: int, H: int, max_q: int, mask_kind: int,
+                            window: int, softmax_scale: float, q: int, q_stride: int, cu_q: int, kv_lens: int,
+                            block_table: int, table_stride: int, max_pages: int, o: int, lse: int, workspace: int,
+                            workspace_bytes: int, stream: int) -> int:
+    return load().ulysses_paged_attn8_fwd(_mref(cache), B, T, H, max_q, mask_kind, window, softmax_scale, q, q_stride,
+                                          cu_q, kv_lens, block_table, table_stride, max_pages, o, lse, workspace,
+                                          workspace_bytes, stream)
 
 
 def ulysses_qk_rope_fwd(shape: Shape, io_layout: int, rope: Optional[RopeStruct], pos0: int, q: int, k: int, w_q: int, w_k: int,
@@ -538,7 +564,7 @@ def attn_bwd(q, k, v, o, lse, do, P: int, mask: Mask, layout: int = LAYOUT_TOKEN
 
 # The helpers of the paged key/value cache are in paged.py, which imports torch; they are brought in when one of
 # them is first asked for.
-_PAGED = ("PagedCache", "page_plan", "kv_append", "paged_attn_workspace", "paged_attn_fwd")
+_PAGED = ("PagedCache", "PagedCache8", "page_plan", "kv_append", "paged_attn_workspace", "paged_attn_fwd")
 
 
 # Those of the rotary calls are in rope.py.

@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 namespace ulysses {
 
@@ -489,6 +490,35 @@ __device__ __forceinline__ float4 ld_shared_v4f(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
                  : "memory");
     return v;
+}
+
+// 2^n for n of [-126, 127].
+__device__ __forceinline__ float pow2f(int n) { return __uint_as_float(uint32_t(n + 127) << 23); }
+
+// The larger magnitudes of two bf16 pairs, without signs, element by element; a NaN in b loses. a has no signs.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    const uint32_t x = b & 0x7fff7fffu;
+    const __nv_bfloat162 m = __hmax2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(x));
+    return reinterpret_cast<const uint32_t&>(m);
+}
+
+// Four e4m3 codes as two fp16 pairs, exactly: the lower two and the upper two.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(c));
+}
+
+// Four 8x8 matrices of 16-bit elements from shared memory, as they lie or transposed.
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
 // Pairs of fp32 values in one instruction.

@@ -28,6 +28,15 @@ bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* bas
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr);
 }
 
+bool encode_code_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows) {
+    cuuint64_t dims[5] = {cuuint64_t(c.d_h), cuuint64_t(c.page_size), cuuint64_t(c.H_kv), cuuint64_t(c.num_pages), 1};
+    cuuint64_t strides[4] = {cuuint64_t(c.token_stride), cuuint64_t(c.head_stride), cuuint64_t(c.page_stride), cuuint64_t(c.page_stride)};
+    cuuint32_t box[5] = {cuuint32_t(c.d_h), cuuint32_t(rows), 1, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, estr,
+                             c.d_h == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // Behind the decode kernel alone one block joins a whole unit, of up to a dozen pieces and more; with the
 // chunk kernel, whose units are 256 rows of mostly two or three pieces, smaller blocks that read two at a
 // time keep more of them in flight (a chunk call of 1.2 PFLOP/s: 237 us, against 243 us with eight).
@@ -72,7 +81,9 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     if (!p.err) return ULYSSES_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const int d = a.cache.d_h, sms = device_sm_count();
-    const bool only = decode_only(p.G, a.max_q);
+    const bool codes = a.scales.k != nullptr;
+    const bool only = decode_only(p.G, a.max_q) || codes;
+    if (codes && !decode_fits(p.G)) return ULYSSES_ERR_UNSUPPORTED;
     PagedParts decode{}, chunk{};
     size_t bytes = 0;
     const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > 3 * sms;
@@ -81,7 +92,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
         p.unit_tokens = paged_decode_rows() / p.G;
         p.parts = decode = paged_decode_parts(ws, d, sms, &bytes);
-        const int rc = launch_paged_decode(a, p, stream);
+        const int rc = codes ? launch_paged_decode8(a, p, stream) : launch_paged_decode(a, p, stream);
         if (rc != ULYSSES_OK) return rc;
         p.min_rows = paged_decode_rows() + 1;
     }

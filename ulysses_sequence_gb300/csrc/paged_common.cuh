@@ -422,12 +422,16 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const PagedParams p, con
 // of `rows` tokens of one page and head by `chunks` chunks (chunk after chunk), 128-byte swizzle.
 bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows, int chunks);
 
+// The same of an 8-bit pool's codes, (d elements, token, head, page), swizzled by the row's length.
+bool encode_code_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows);
+
 // Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu): where their pieces lie in a
 // workspace on a device of `sms` SMs (`bytes` of it, whatever the device), and their launches.
 int paged_decode_rows();
 PagedParts paged_decode_parts(void* workspace, int d_h, int sms, size_t* bytes);
 PagedParts paged_chunk_parts(void* workspace, int d_h, int sms, size_t* bytes);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
+int launch_paged_decode8(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
 int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream);
 
 // Pieces of `most` CTAs at the front of a workspace, for a launch of `ctas` of them.

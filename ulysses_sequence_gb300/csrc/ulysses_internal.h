@@ -35,11 +35,11 @@ inline KvInfo kv_info(const ulysses_shape_t& s) {
     return k;
 }
 
-// cuTensorMapEncodeTiled (looked up at run time) with the 128-byte swizzle, 256-byte L2
-// promotion and zero fill out of bounds.
+// cuTensorMapEncodeTiled (looked up at run time) with the 128-byte swizzle (or the one given), 256-byte
+// L2 promotion and zero fill out of bounds.
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
                        const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                       const cuuint32_t* elem_strides);
+                       const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Encodes a 5-D bf16 tensor map over (d, head, row, batch, unit) with a box of
 // (64, 1, box_rows, 1, 1), 128-byte swizzle and zero fill out of bounds, for a tensor with
@@ -149,9 +149,20 @@ int launch_page_plan(int B, int T, int page_shift, int max_pages, int64_t table_
 int launch_kv_append(const ulysses_kv_cache_t& c, int T, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, const int32_t* slots, cudaStream_t stream);
 
+// The scales of an 8-bit cache: bytes [page][block][head], exponents plus 127.
+struct PagedScales {
+    const uint8_t *k, *v;  // nullptr: the cache is bf16
+    int block_shift;       // log2 of a block's tokens
+};
+// Common form of both caches: for 8 bits k and v are codes of one byte, strides in elements either way.
+ulysses_kv_cache_t plain_form(const ulysses_kv_cache8_t& c);
+int launch_kv_append8(const ulysses_kv_cache8_t& c, int T, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const int32_t* slots, cudaStream_t stream);
+
 // One paged attention call, validated.
 struct PagedAttnArgs {
     ulysses_kv_cache_t cache;
+    PagedScales scales;
     int B, T, H, max_q, window;
     bool causal;
     float scale;

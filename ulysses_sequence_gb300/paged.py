@@ -23,6 +23,7 @@ import torch
 import ulysses_sequence_gb300 as U
 
 _I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _INT_MAX = 2 ** 31 - 1  # of the C ABI's int arguments, which ctypes would wrap
 # The short cuts behind torch.cuda.current_device() and current_stream().cuda_stream (an append of 64 rows takes the
 # host 4.6 us with them and 6.1 us without), where this build of torch has them.
@@ -86,6 +87,8 @@ class PagedCache:
     """A pool of key/value pages for the C ABI: k and v bf16 [num_pages][page_size][H_kv][d] with equal
     strides and contiguous heads (any order of the first three dimensions in memory)."""
 
+    codes = False
+
     def __init__(self, k, v):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
             raise ValueError("PagedCache: k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
@@ -104,6 +107,47 @@ class PagedCache:
     def empty(num_pages: int, page_size: int, H_kv: int, d: int, device="cuda") -> "PagedCache":
         """A pool in the token layout, its contents undefined (unwritten entries are never used)."""
         return PagedCache(*(torch.empty((num_pages, page_size, H_kv, d), dtype=_BF16, device=device) for _ in range(2)))
+
+
+class PagedCache8:
+    """A pool of key/value pages in 8 bits for the C ABI: k and v float8_e4m3fn [num_pages][page_size][H_kv][d], strided like
+    PagedCache's, and k_scale and v_scale float8_e8m0fnu [num_pages][page_size / block][H_kv] contiguous, one power of
+    two for each `block` tokens of a page and head: key = k * k_scale. Scales lie in [2^-117, 2^119]."""
+
+    codes = True
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("PagedCache8: k and v must have the same shape [num_pages][page_size][H_kv][d] and strides")
+        if k.dtype != _E4M3 or v.dtype != _E4M3 or k.stride(3) != 1:
+            raise ValueError("PagedCache8: k and v must be float8_e4m3fn with contiguous heads")
+        if max(k.shape) > _INT_MAX:
+            raise ValueError(f"PagedCache8: sizes must fit 32 bits, got {tuple(k.shape)}")
+        pages, page, H_kv, _ = k.shape
+        blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if x.dtype != _E8M0 or blocks < 1 or x.shape != (pages, blocks, H_kv) or page % blocks or not x.is_contiguous():
+                raise ValueError(f"PagedCache8: {name} must be contiguous float8_e8m0fnu [{pages}][blocks that divide {page}][{H_kv}], got "
+                                 f"{x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+        if not k.is_cuda or any(x.device != k.device for x in (v, k_scale, v_scale)):
+            raise ValueError("PagedCache8: k, v and their scales must be on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.get_device()
+        self.num_pages, self.page_size, self.H_kv, self.d = k.shape
+        self.block = page // blocks
+        self.struct = U.KVCache8Struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *k.shape, k.stride(0),
+                                       k.stride(1), k.stride(2), self.block)
+        self.ref = ctypes.byref(self.struct)
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, H_kv: int, d: int, block: Optional[int] = None, device="cuda") -> "PagedCache8":
+        """A pool in the token layout, its codes undefined (unwritten entries are never used), its scales the smallest; one
+        scale a page and head unless `block` says how many tokens share one."""
+        block = page_size if block is None else block
+        if block < 1 or page_size % block:
+            raise ValueError(f"PagedCache8: block must divide page_size {page_size}, got {block}")
+        kv = (torch.empty((num_pages, page_size, H_kv, d), dtype=torch.uint8, device=device).view(_E4M3) for _ in range(2))
+        scales = (torch.full((num_pages, page_size // block, H_kv), 10, dtype=torch.uint8, device=device).view(_E8M0) for _ in range(2))
+        return PagedCache8(*kv, *scales)
 
 
 def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size: int, num_pages: int, T: int, cu_q=None,
@@ -160,9 +204,12 @@ def page_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size:
     return cu_q, kv_lens, slot_map, info
 
 
-def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
+def kv_append(k, v, cache, slot_map, stream=None) -> None:
     """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
-    fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped."""
+    fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped.
+    Into a PagedCache8 they are rounded to codes, and the scales of their blocks are set (a block that begins with one
+    of them) or grown, its older tokens rounded again; rows of one block must then follow one another, as page_plan
+    places them."""
     where, dev = "kv_append", cache.device
     T = k.shape[0] if k.dim() else 0
     if T > _INT_MAX:
@@ -172,13 +219,14 @@ def kv_append(k, v, cache: PagedCache, slot_map, stream=None) -> None:
     if not (slot_map.shape == (T,) and slot_map.dtype is _I32 and slot_map.get_device() == dev
             and slot_map.is_contiguous()):
         _refuse(slot_map, "slot_map", (T,), _I32, dev, where)
-    rc = U.load().ulysses_kv_append(cache.ref, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
-                                    _stream_of(dev, stream, where))
+    lib = U.load()
+    append = lib.ulysses_kv_append8 if cache.codes else lib.ulysses_kv_append
+    rc = append(cache.ref, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(), _stream_of(dev, stream, where))
     if rc:
         U.check(rc, where)
 
 
-def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
+def paged_attn_workspace(q, cache, max_q: int = 0):
     """Workspace of paged_attn_fwd for q [T][H][d]; its size depends on H, d and max_q alone, so one serves every
     step of a program. Calls that may overlap on the GPU need one each."""
     if not -1 <= max_q <= _INT_MAX:
@@ -189,10 +237,10 @@ def paged_attn_workspace(q, cache: PagedCache, max_q: int = 0):
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
-def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int = 0, mask: Optional["U.Mask"] = None,
+def paged_attn_fwd(q, cache, cu_q, kv_lens, block_table, max_q: int = 0, mask: Optional["U.Mask"] = None,
                    window: int = 0, scale: float = 0.0, o=None, lse=None, workspace=None, stream=None):
     """Attention of packed new tokens q bf16 [T][H][d] (request i owns rows cu_q[i] .. cu_q[i+1]) over the pages that
-    block_table [B][max_pages] names, kv_lens[B] keys each, the new tokens last. mask: Mask.causal() (the default)
+    block_table [B][max_pages] of a PagedCache or PagedCache8 names, kv_lens[B] keys each, the new tokens last. mask: Mask.causal() (the default)
     by position, with an optional sliding window, or Mask.none(). max_q bounds the new tokens of a request where
     known (1 when decoding; 0: unknown). Returns (o bf16 [T][H][d], lse fp32 [H][T]); rows behind the last
     request are left as they were."""
@@ -225,10 +273,11 @@ def paged_attn_fwd(q, cache: PagedCache, cu_q, kv_lens, block_table, max_q: int 
         workspace = _new((max(n, 256),), torch.uint8, dev, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous on device {dev}")
-    rc = U.load().ulysses_paged_attn_fwd(cache.ref, B, T, H, max_q, U.MASK_CAUSAL if mask is None else mask.kind, window,
-                                         scale, q.data_ptr(), q_stride, cu_q.data_ptr(), kv_lens.data_ptr(),
-                                         block_table.data_ptr(), table_stride, width, o.data_ptr(), lse.data_ptr(),
-                                         workspace.data_ptr(), workspace.nbytes, st)
+    lib = U.load()
+    attn = lib.ulysses_paged_attn8_fwd if cache.codes else lib.ulysses_paged_attn_fwd
+    rc = attn(cache.ref, B, T, H, max_q, U.MASK_CAUSAL if mask is None else mask.kind, window, scale, q.data_ptr(), q_stride,
+              cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), table_stride, width, o.data_ptr(), lse.data_ptr(),
+              workspace.data_ptr(), workspace.nbytes, st)
     if rc:
         U.check(rc, where)
     return o, lse
