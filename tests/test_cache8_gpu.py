@@ -266,10 +266,117 @@ def test_queries_of_very_different_elements():
     s.check(max_q=40)
 
 
-def test_same_bits_every_time():
-    s = Step8([(1, c) for c in (3000, 10, 700)], 8, 2, 128, 16, seed=1)
-    a, b = s.run(1), s.run(1)
+@pytest.mark.parametrize("mask,window", [("causal", 0), ("none", 0), ("causal", 1), ("causal", 37), ("causal", 128), ("causal", 2 ** 31 - 1)])
+@pytest.mark.parametrize("H,Hkv,d,page,block", [(8, 2, 128, 32, 32), (2, 2, 64, 16, 16), (8, 2, 128, 256, 64)])
+def test_masks_in_a_mixed_batch(mask, window, H, Hkv, d, page, block):
+    reqs = [(1, 500), (0, 40), (140, 0), (1, 0), (0, 0), (70, 333), (3, 129), (1, 127), (33, 700)]
+    Step8(reqs, H, Hkv, d, page, block, seed=window % 1000, pad=5).check(max_q=140, mask=mask, window=window)
+
+
+@pytest.mark.parametrize("H,d,n", [(32, 128, 6), (32, 64, 6), (16, 128, 70), (16, 64, 70)])
+def test_many_key_tiles_in_a_row(H, d, n):
+    """Units of one and of two row tiles with twenty and more key tiles to a CTA, in batches that fill the grid."""
+    rng = np.random.default_rng(H + d + n)
+    reqs = [(n, int(c)) for c in rng.integers(1800, 3000, 20 if n < 10 else 3)]
+    Step8(reqs, H, 8, d, 64, 32, seed=d + n).check(max_q=n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_of_one_and_of_two_tiles_in_turn(d):
+    rng = np.random.default_rng(d)
+    reqs = [(int(rng.integers(5, 33)) if i % 3 else int(rng.integers(40, 65)), int(rng.integers(0, 900))) for i in range(260)]
+    Step8(reqs, 8, 2, d, 32, seed=d).check()
+
+
+@pytest.mark.parametrize("H,n", [(17, 20), (100, 3), (128, 5)])
+def test_more_heads_to_a_key_than_a_decode_tile(H, n):
+    Step8([(n, 140), (1, 600)], H, 1, 64, 32, seed=H, pad=1).check(max_q=n)
+
+
+@pytest.mark.parametrize("B,n,max_q", [(257, 1, 1), (257, 23, 23), (700, 1, 0)])
+def test_many_requests(B, n, max_q):
+    rng = np.random.default_rng(B + n)
+    Step8([(0 if i % 9 == 4 else n, int(c)) for i, c in enumerate(rng.integers(0, 60, B))], 2, 1, 64, 16, seed=B, pad=2).check(max_q=max_q)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mask,window", [("causal", 0), ("causal", 90), ("none", 0)])
+def test_mixed_batch_that_takes_both_kernels(d, mask, window):
+    rng = np.random.default_rng(window + d)
+    reqs = [(0 if i % 13 == 6 else int(rng.integers(9, 70)) if i % 10 == 3 else 1, int(rng.integers(0, 300))) for i in range(60)]
+    s = Step8(reqs, 16, 8, d, 16, seed=window, pad=4)
+    s.check(max_q=70, mask=mask, window=window)
+    s.check(max_q=0, mask=mask, window=window)
+
+
+@pytest.mark.parametrize("n", [40, 130])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_equal_the_bf16_cache_of_the_same_values(n, d):
+    """Codes times scales are exact in bf16, and the chunk kernels multiply them in the same order: the same bits."""
+    s = Step8([(n, 700), (n, 3), (n + 1, 90)], 8, 2, d, 32, 16, seed=n)
+    k, v = (torch.nan_to_num(x).to(torch.bfloat16).cuda() for x in (s.k, s.v))
+    a = s.run(n + 1)
+    s.cache = U.PagedCache(k, v)
+    b = s.run(n + 1)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("n", [1, 50])
+def test_same_bits_every_time(n):
+    s = Step8([(n, c) for c in (3000, 10, 700)], 8, 2, 128, 16, seed=1)
+    a, b = s.run(n), s.run(n)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_nan_keys_and_values(n):
+    """NaN among a request's keys makes rows that see it NaN in o and lse; among its values, in those elements of o."""
+    s = Step8([(n, 60), (n, 300)], 4, 2, 64, 16, seed=n)
+    (kc, ks), (vc, vs) = s.parts
+    t = 30  # a cached token of either request, in key/value head 1
+    page0, page1 = int(s.table[0, t // 16]), int(s.table[1, t // 16])
+    kc[page0, t % 16, 1, 9] = 0x7f
+    vc[page1, t % 16, 1, 5] = 0xff
+    s.put()
+    o, lse = s.run(n)
+    healthy()
+    assert torch.isnan(o[:n, 2:]).all() and torch.isnan(lse[2:, :n]).all()
+    assert torch.isfinite(o[:n, :2]).all() and torch.isfinite(lse[:2]).all() and torch.isfinite(lse[:, n:]).all()
+    bad = torch.isnan(o[n:])
+    assert bad[:, 2:, 5].all() and int(bad.sum()) == 2 * n
+
+
+def test_two_graphs_share_a_workspace():
+    a, b = Step8([(1, 3000), (1, 40)], 8, 2, 128, 16, seed=41), Step8([(150, 700), (1, 900), (0, 5)], 8, 2, 128, 16, seed=42)
+    ws = U.paged_attn_workspace(b.q, b.cache, 0)
+    calls = []
+    for x, max_q in ((a, 1), (b, 150)):
+        args = (x.q, x.cache, i32(x.cu), i32(x.kv), i32(x.table), max_q)
+        want = [t.clone() for t in U.paged_attn_fwd(*args)]
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            U.paged_attn_fwd(*args, o=o, lse=lse, workspace=ws)
+        calls.append((graph, o, lse, want, args))
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        graph, o, lse, want, _ = calls[i]
+        o.fill_(0)
+        graph.replay()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    healthy()
+
+
+def test_another_stream_and_two_at_once():
+    a, b = Step8([(1, 3000)] * 4, 8, 2, 128, 16, seed=11), Step8([(70, 900)] * 3, 8, 2, 128, 16, seed=12)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    args = [(x.q, x.cache, i32(x.cu), i32(x.kv), i32(x.table), x.new[0]) for x in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [U.paged_attn_fwd(*x, stream=st) for x, st in zip(args, (sa, sb))]
+    torch.cuda.synchronize()
+    for x, (o, lse) in zip((a, b), got):
+        hold(o, lse, x.oracle(), 128)
 
 
 # ------------------------------------------------------------------ as they are used

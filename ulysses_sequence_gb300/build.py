@@ -23,7 +23,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
               "-I" + os.path.join(ROOT, "include")] + ARCH
 SOURCES = ["api.cu", "relayout.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_noalloc.cu", "proj.cu", "usp.cu",
            "paged_api.cu", "paged_plan.cu", "paged_attn.cu", "paged_decode.cu",
-           "paged_chunk.cu", "paged_append8.cu", "paged_decode8.cu", "rope_api.cu", "rope.cu"]
+           "paged_chunk.cu", "paged_append8.cu", "paged_decode8.cu", "paged_chunk8.cu",
+           "rope_api.cu", "rope.cu"]
 
 
 def nvcc() -> str:

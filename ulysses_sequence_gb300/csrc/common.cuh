@@ -9,6 +9,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+// The waits' slow paths are functions of their own, which keeps the kernels short. A kernel that moves registers between
+// its warpgroups cannot call functions (each would need the fewest registers of any caller) and defines this as inline.
+#ifndef ULYSSES_SLOW_PATH
+#define ULYSSES_SLOW_PATH __noinline__
+#endif
+
 namespace ulysses {
 
 // ---------------------------------------------------------------------------------------
@@ -77,7 +83,7 @@ __device__ __forceinline__ void record_error(uint32_t* err, uint32_t code) {
 
 // Waits for the phase with the given parity to complete. Returns false (and makes sure
 // the CTA's abort flag is set) if the CTA is aborting or the wait exceeded its limit.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Abort ab, uint32_t role,
+static __device__ ULYSSES_SLOW_PATH bool mbar_wait_slow(uint32_t bar, uint32_t parity, Abort ab, uint32_t role,
                                             uint32_t site) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
@@ -103,7 +109,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, Abort 
 
 // A bounded wait that ignores the abort flag: used only to drain copies and MMAs already
 // in flight before a CTA leaves, after an abort or whatever the other roles have seen.
-static __device__ __noinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+static __device__ ULYSSES_SLOW_PATH void mbar_drain(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(a, parity)) {
@@ -418,7 +424,7 @@ __device__ __forceinline__ bool mbar_try_wait_cl(uint32_t bar, uint32_t parity) 
     return ok != 0;
 }
 // bounded wait with cluster-scope acquire (barriers that other CTAs arrive on)
-static __device__ __noinline__ bool mbar_wait_cl(uint64_t* barp, uint32_t parity, Abort ab, uint32_t role,
+static __device__ ULYSSES_SLOW_PATH bool mbar_wait_cl(uint64_t* barp, uint32_t parity, Abort ab, uint32_t role,
                                                  uint32_t site) {
     const uint32_t bar = smem_u32(barp);
     if (mbar_try_wait_cl(bar, parity)) return true;
@@ -527,6 +533,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
         : "=l"(reinterpret_cast<uint64_t&>(d))
         : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

@@ -82,8 +82,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const int d = a.cache.d_h, sms = device_sm_count();
     const bool codes = a.scales.k != nullptr;
-    const bool only = decode_only(p.G, a.max_q) || codes;
-    if (codes && !decode_fits(p.G)) return ULYSSES_ERR_UNSUPPORTED;
+    const bool only = decode_only(p.G, a.max_q);
     PagedParts decode{}, chunk{};
     size_t bytes = 0;
     const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > 3 * sms;
@@ -100,7 +99,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
         p.max_rows = 0x7fffffff;
         p.unit_tokens = 2 * (kTile / p.G);
         p.parts = chunk = paged_chunk_parts(ws + bytes, d, sms, &bytes);
-        const int rc = launch_paged_chunk(a, p, both, stream);
+        const int rc = codes ? launch_paged_chunk8(a, p, both, stream) : launch_paged_chunk(a, p, both, stream);
         if (rc != ULYSSES_OK) return rc;
     }
     return d == 128 ? launch_join<128>(p, decode, chunk, stream) : launch_join<64>(p, decode, chunk, stream);

@@ -433,6 +433,7 @@ PagedParts paged_chunk_parts(void* workspace, int d_h, int sms, size_t* bytes);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
 int launch_paged_decode8(const PagedAttnArgs& a, const PagedParams& p, cudaStream_t stream);
 int launch_paged_chunk(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream);
+int launch_paged_chunk8(const PagedAttnArgs& a, const PagedParams& p, bool behind_decode, cudaStream_t stream);
 
 // Pieces of `most` CTAs at the front of a workspace, for a launch of `ctas` of them.
 inline PagedParts paged_parts(void* workspace, int most, int ctas, int rows, int d_h, size_t* bytes) {
