@@ -2,18 +2,17 @@
 // of products these are).
 //
 // The products run in bf16: every key and value of such a cache, code x power of two, is exact in bf16, so nothing is
-// rounded that attention over a bf16 cache would not round, and queries stay as they are. Four converter warps stand where
-// the bulk copies of keys and values are there: they read codes from global memory a tile ahead into registers, turn them
-// into scaled bf16 (e4m3 pair -> fp16 pair -> two fp32, times the scale -> bf16 pair) and write them into the swizzled
-// operand tiles. Codes make no trip through shared memory of their own, whose bandwidth the products need. Warp roles (512
-// threads, a warpgroup each; registers are moved from the first and the last to the two between):
-//   warp 0       producer: walks the share, looks up pages and scales (one lane to 16 keys) and publishes each piece and each
-//                tile; brings the queries;
+// rounded that attention over a bf16 cache would not round, and queries stay as they are. Codes come into a small ring of
+// shared memory by bulk copies; four converter warps turn them into scaled bf16 (e4m3 pair -> fp16 pair -> two fp32, times
+// the scale -> bf16 pair) in the swizzled operand tiles. Warp roles (512 threads, a warpgroup each; registers are moved from
+// the first and the last to the two between):
+//   warp 0       producer: walks the share, looks up pages and scales (one lane to 16 keys), copies codes and queries, and
+//                publishes each piece and each tile;
 //   warp 1       MMA issuer;
 //   warps 4-7    softmax of tile 0, warps 8-11 of tile 1;
 //   warps 12-15  converters: 32 keys of every tile each. Values behind the request's last key become zeros (0 x NaN is NaN).
-// A converter reads a row's 16 codes with one lane, and eight lanes that write at once take four pieces of each of two rows
-// whose numbers differ in the lowest bit, which the swizzle puts on different banks.
+// A converter reads a row's 16 codes with one lane; eight lanes that read and write at once take four pieces of each of two
+// rows whose numbers differ in the bits that the swizzles of codes and of bf16 put on different banks.
 #define ULYSSES_SLOW_PATH __forceinline__
 #include "paged_common.cuh"
 
@@ -25,25 +24,27 @@ constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 2 * kTile;
 constexpr int kChunkMinCost = 4;     // the smallest share of a CTA, in key tiles
 constexpr int kChunkUnitCost = 3;    // the fixed cost of a unit, in key tiles
-constexpr int kLead = 4;             // tiles that the producer is ahead of the converters at most
 // Registers of a thread by warpgroup: 512 threads are launched with 128 each.
 constexpr uint32_t kRegsIssue = 72, kRegsSoftmax = 176, kRegsConvert = 88;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "no more than the launch brought");
 
 template <int D>
 struct Chunk8Cfg {
-    static constexpr int NSK = D == 64 ? 4 : 3;  // K and V pipeline stages
+    static constexpr int NSC = D == 64 ? 6 : 2;  // stages of codes, keys and values in turn
+    static constexpr int NSK = D == 64 ? 4 : 2;  // of K and V in bf16
     static constexpr int NSV = D == 64 ? 4 : 2;
     static constexpr int RING = D == 64 ? 16 : 8;  // tile descriptions
+    static constexpr uint32_t CODE_BYTES = kTile * D;
     static constexpr uint32_t TILE_BYTES = kTile * D * 2;
     static constexpr uint32_t CHUNK_BYTES = kTile * 128;  // 128 rows x 64 elements, swizzled
     static constexpr uint32_t OFF_K = 2 * TILE_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + NSK * TILE_BYTES;
-    static constexpr uint32_t OFF_PIECE = OFF_V + NSV * TILE_BYTES;
+    static constexpr uint32_t OFF_C = OFF_V + NSV * TILE_BYTES;
+    static constexpr uint32_t OFF_PIECE = OFF_C + NSC * CODE_BYTES;
     static constexpr uint32_t OFF_INFO = OFF_PIECE + 128;
     static constexpr uint32_t OFF_SH = OFF_INFO + RING * 128;
     static constexpr uint32_t OFF_BAR = OFF_SH + 192;
-    static constexpr int BARS = 17 + 2 * (NSK + NSV + RING);
+    static constexpr int BARS = 17 + 2 * (NSC + NSK + NSV) + RING;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 640 + 1024;
     static_assert((kChunkThreads / 32 + 2) * 8 <= 192 && BARS * 8 + 8 <= 640, "room for the shares and the barriers");
     static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
@@ -53,18 +54,18 @@ struct Chunk8Cfg {
     static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory");
     // the issuer names columns from 0, constants of its instructions: true of an allocation of the whole tensor memory
     static_assert(TMEM_COLS == 512, "the allocation starts at column 0");
-    // Tile n is published once tile n - kLead is converted, for which the scores of tile n - kLead - NSK were done: the
-    // softmax warps then have read what describes the tile before that one (with AHEAD the one before it).
-    static_assert(kLead + NSK + (AHEAD ? 1 : 0) < RING, "tile descriptions outlive their readers");
+    // Tile n is published when the stage of its keys' codes is free: those of tile n - NSC / 2 are converted, for which the
+    // scores of tile n - NSC / 2 - NSK were done, and the softmax warps have read what describes the tile before that one
+    // (with AHEAD the one before it).
+    static_assert(NSC % 2 == 0 && NSC / 2 + NSK + (AHEAD ? 1 : 0) < RING, "tile descriptions outlive their readers");
 };
 
 // One key tile.
 struct ChunkTile {
     uint32_t what;     // kInfoMasked and the pages that exist; kInfoEnd: no tile, the share is done
-    int key0, head;    // first key, key/value head
-    int limit;         // keys of the request from key0 on
-    int page[8];       // of keys [16 i, 16 i + 16), -1 where there is none
-    float k[8], v[8];  // their scales
+    int limit;         // keys of the request from its first key on
+    int pad[2];
+    float k[8], v[8];  // scales of keys [16 i, 16 i + 16)
 };
 static_assert(sizeof(ChunkTile) <= 128, "tile ring");
 
@@ -79,13 +80,6 @@ static_assert(2 * sizeof(ChunkPiece) <= 128, "piece ring");
 
 constexpr uint32_t kInfoEnd = 0x200;
 constexpr uint32_t kInfoMasked = 0x100;  // some row does not see all of the tile; bits 0-7: pages of 16 keys that exist
-
-// The codes and where they lie (strides in bytes).
-struct Chunk8Pool {
-    const uint8_t *k, *v;
-    int64_t page_stride, token_stride, head_stride;
-    PagedScales scales;
-};
 
 // 16 codes as bf16 times a power of two, exactly: two pieces of 8.
 __device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, uint4& hi) {
@@ -112,12 +106,14 @@ __device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, 
 // released this one.
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams p, const Chunk8Pool pool, int behind_decode) {
+paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const PagedScales scales,
+                    int log_rows /* of one page copy */, int behind_decode) {
     using C = Chunk8Cfg<D>;
     constexpr int NSK = C::NSK, NSV = C::NSV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
+    uint8_t *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V, *sC = smem + C::OFF_C;
     ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + C::OFF_PIECE);  // [2]
     auto tile_info = [&](int n) { return reinterpret_cast<ChunkTile*>(smem + C::OFF_INFO + (n % C::RING) * 128); };
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -132,8 +128,9 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
     uint64_t* piece_full = o_done + 2;      // [2]
     uint64_t* piece_empty = piece_full + 2; // [2], MMA issuer and eight softmax warps
     uint64_t* info_full = piece_empty + 2;  // [RING]
-    uint64_t* info_done = info_full + C::RING;  // [RING], the converter warps
-    uint64_t* drain = info_done + C::RING;
+    uint64_t* c_full = info_full + C::RING;  // [NSC]
+    uint64_t* c_empty = c_full + C::NSC;     // [NSC], the converter warps
+    uint64_t* drain = c_empty + C::NSC;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -159,9 +156,10 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
             mbar_init(piece_full + t, 1);
             mbar_init(piece_empty + t, 9);
         }
-        for (int i = 0; i < C::RING; ++i) {
-            mbar_init(info_full + i, 1);
-            mbar_init(info_done + i, 4);
+        for (int i = 0; i < C::RING; ++i) mbar_init(info_full + i, 1);
+        for (int i = 0; i < C::NSC; ++i) {
+            mbar_init(c_full + i, 1);
+            mbar_init(c_empty + i, 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -192,30 +190,45 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
     regs_dec<kRegsIssue>();
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
-        if (lane == 0) tma_prefetch_desc(&tm_q);
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
         if (p.B <= kLaneRequests) paged_share_lanes(p, kChunkMinCost, w);
         else if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
-        // lanes 0 to 7 look up the pages of 16 keys each and the keys' scales, lanes 8 to 15 the same for the values' scales
+        // lane l of the first 16 looks up the page of keys [16 (l % 8), + 16), and the scale of the keys (l < 8) or values
+        // there; the first of a copy's lanes issues it
         const int my_key = (lane & 7) * 16;
+        const bool copies = lane < 8 && (my_key & ((1 << log_rows) - 1)) == 0;
         auto lookup = [&](int key0) {
             const int key = key0 + my_key;
             const int id = lane < 16 && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
             return unsigned(id) < unsigned(p.num_pages) ? id : -1;
         };
-        const uint8_t* scale_of = lane < 8 ? pool.scales.k : pool.scales.v;
+        const uint8_t* scale_of = lane < 8 ? scales.k : scales.v;
         auto scale = [&](int id, int key0) {
             if (id < 0) return 127;
             const int token = (key0 + my_key) & ((1 << p.page_shift) - 1);
-            const int64_t at = (int64_t(id) << (p.page_shift - pool.scales.block_shift)) + (token >> pool.scales.block_shift);
+            const int64_t at = (int64_t(id) << (p.page_shift - scales.block_shift)) + (token >> scales.block_shift);
             return int(scale_of[at * p.Hkv + w.head]);
         };
         PagedMeta meta{0, 0, 0, 0};
-        int n = 0, nq = 0, piece = 0;  // tiles, copies of queries and pieces so far
+        int n = 0, nc = 0, nq = 0, piece = 0;  // tiles, stages of codes, copies of queries and pieces so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_LOAD, site));
         };
-        auto room = [&] { return n < kLead || wait(info_done + (n - kLead) % C::RING, ((n - kLead) / C::RING) & 1, 2); };
+        auto room = [&](uint32_t site) { return nc < C::NSC || wait(c_empty + nc % C::NSC, ((nc / C::NSC) - 1) & 1, site); };
+        auto copy = [&](const CUtensorMap* map, int id, int key0) {
+            const int st = nc++ % C::NSC;
+            if (lane == 0) mbar_arrive_expect_tx(c_full + st, C::CODE_BYTES);
+            __syncwarp();
+            // a page that does not exist is copied from behind the pool: zeros
+            if (copies)
+                tma_load_5d(sC + st * C::CODE_BYTES + my_key * D, map, c_full + st, 0, (key0 + my_key) & ((1 << p.page_shift) - 1),
+                            w.head, id >= 0 ? id : p.num_pages, 0);
+        };
         while (ok && w.left > 0) {
             // the next piece: what this CTA does of the walk's unit
             int off, tiles;
@@ -243,25 +256,21 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
             for (int i = 0; i < tiles; ++i) {
                 const int key0 = key_first + i * kTile;
                 const int id_next = i + 1 < tiles ? lookup(key0 + kTile) : -1;
-                if (!(ok = room())) break;
+                if (!(ok = room(2))) break;
                 const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0) & 0xffu;
                 ChunkTile* t = tile_info(n);
-                if (lane < 16) {
-                    (lane < 8 ? t->k : t->v)[lane & 7] = __uint_as_float(uint32_t(byte) << 23);
-                    if (lane < 8) t->page[lane] = id;
-                }
+                if (lane < 16) (lane < 8 ? t->k : t->v)[lane & 7] = __uint_as_float(uint32_t(byte) << 23);
                 if (lane == 0) {
                     // clear: every row of the unit sees every key of the tile
                     const bool clear = valid == 0xff && key0 + kTile <= w.s.kv &&
                                        (!p.causal || (key0 + kTile <= pos + 1 && (p.window == 0 || key0 > pos + tokens - 1 - p.window)));
                     t->what = valid | (clear ? 0u : kInfoMasked);
-                    t->key0 = key0;
-                    t->head = w.head;
                     t->limit = w.s.kv - key0;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(info_full + n % C::RING);
                 ++n;
+                copy(&tm_k, id, key0);
                 if (i == 0) {
                     // the unit's queries, once the previous piece's last scores are computed
                     if (piece >= 1 && !(ok = wait(q_empty, (piece - 1) & 1, 3))) break;
@@ -276,6 +285,8 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
                     __syncwarp();
                     ++nq;
                 }
+                if (!(ok = room(4))) break;
+                copy(&tm_v, id, key0);
                 id = id_next;
                 byte = scale(id, key0 + kTile);
             }
@@ -283,7 +294,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
             ++piece;
             if (w.left > 0) w.next_unit(p);
         }
-        if (ok && (ok = room()) && lane == 0) {
+        if (ok && (ok = room(6)) && lane == 0) {
             tile_info(n)->what = kInfoEnd;
             mbar_arrive(info_full + n % C::RING);
         }
@@ -295,6 +306,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
             p.parts.meta[cta] = meta;
             // every copy lands before the CTA can exit, also where another role has given up since
             ring_drain<1>(q_full, nq);
+            ring_drain<C::NSC>(c_full, nc);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
@@ -388,28 +400,25 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
         // this lane's row within 8, and its 16 codes within 64
         const int my_row = cw * 32 + (D == 128 ? ((lane & 4) ? quarter ^ 5 : quarter) : 2 * quarter + ((lane >> 2) & 1));
         const int my_unit = lane & 3;
-        bool ok = true;
+        int nc = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_LOAD, site));
         };
-        auto load = [&](const uint8_t* base, const ChunkTile* t, uint4 (*x)[D / 64]) {
+        // one tile of keys or values: all its codes first, so that no unit's loads stand behind another's stores
+        uint4 x[4][D / 64];
+        auto load = [&] {
+            const uint32_t codes = smem_u32(sC + (nc % C::NSC) * C::CODE_BYTES);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {  // 8 rows each
-                const int page = t->page[cw * 2 + (g >> 1)], token = (t->key0 + my_row + 8 * g) & ((1 << p.page_shift) - 1);
-                const uint8_t* src = base + page * pool.page_stride + token * pool.token_stride + t->head * pool.head_stride + my_unit * 16;
+            for (int g = 0; g < 4; ++g)  // 8 rows each
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    x[g][c] = make_uint4(0, 0, 0, 0);
-                    if (page >= 0) x[g][c] = *reinterpret_cast<const uint4*>(src + c * 64);
-                }
-            }
+                for (int c = 0; c < D / 64; ++c) x[g][c] = ld_shared_v4u(codes + code_offset<D>(my_row + 8 * g, 4 * c + my_unit));
         };
-        auto store = [&](uint8_t* tile, const float* scales, int limit, const uint4 (*x)[D / 64]) {
+        auto store = [&](uint8_t* tile, const float* by, int limit) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int row = my_row + 8 * g;
                 const uint32_t a = smem_u32(tile) + row * 128, sw = row & 7;
-                const float s = scales[cw * 2 + (g >> 1)];
+                const float s = by[cw * 2 + (g >> 1)];
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint4 lo, hi;
@@ -422,26 +431,25 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams 
             fence_proxy_async_smem();
             __syncwarp();
         };
-        uint4 xk[4][D / 64], xv[4][D / 64];
-        ok = wait(info_full, 0, 11);
-        if (ok && !(tile_info(0)->what & kInfoEnd)) load(pool.k, tile_info(0), xk);
-        for (int j = 0; ok; ++j) {
+        for (int j = 0;; ++j) {
+            if (!wait(info_full + j % C::RING, (j / C::RING) & 1, 11)) break;
             const ChunkTile* t = tile_info(j);
             if (t->what & kInfoEnd) break;
-            const int sk = j % NSK, sv = j % NSV;
-            load(pool.v, t, xv);
-            if (j >= NSK && !(ok = wait(k_empty + sk, ((j / NSK) - 1) & 1, 12))) break;
-            store(sK + sk * C::TILE_BYTES, t->k, kTile, xk);
-            if (lane == 0) mbar_arrive(k_full + sk);
-            if (!(ok = wait(info_full + (j + 1) % C::RING, ((j + 1) / C::RING) & 1, 13))) break;
-            const ChunkTile* next = tile_info(j + 1);
-            if (!(next->what & kInfoEnd)) load(pool.k, next, xk);
-            if (j >= NSV && !(ok = wait(v_empty + sv, ((j / NSV) - 1) & 1, 14))) break;
-            store(sV + sv * C::TILE_BYTES, t->v, t->limit, xv);
-            if (lane == 0) {
-                mbar_arrive(v_full + sv);
-                mbar_arrive(info_done + j % C::RING);
+            bool ok = true;
+#pragma unroll 1
+            for (int value = 0; value < 2 && ok; ++value, ++nc) {
+                const int ns = value ? NSV : NSK, st = j % ns;
+                uint64_t *full = (value ? v_full : k_full) + st, *empty = (value ? v_empty : k_empty) + st;
+                if (!(ok = wait(c_full + nc % C::NSC, (nc / C::NSC) & 1, 12))) break;
+                load();
+                if (!(ok = j < ns || wait(empty, ((j / ns) - 1) & 1, 13))) break;
+                store((value ? sV : sK) + st * C::TILE_BYTES, value ? t->v : t->k, value ? t->limit : kTile);
+                if (lane == 0) {
+                    mbar_arrive(full);
+                    mbar_arrive(c_empty + nc % C::NSC);
+                }
             }
+            if (!ok) break;
         }
     } else {
         // ------------------------------------------------------------------ softmax (tile t)
@@ -630,11 +638,13 @@ int launch_chunk8_d(const PagedAttnArgs& a, const PagedParams& p, bool behind_de
         cuuint32_t estr[5] = {1, 1, 1, 1, 1};
         if (!encode_tensor_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.q, dims, strides, box, estr)) return ULYSSES_ERR_CUDA;
     }
-    const Chunk8Pool pool{static_cast<const uint8_t*>(a.cache.k), static_cast<const uint8_t*>(a.cache.v), a.cache.page_stride,
-                          a.cache.token_stride, a.cache.head_stride, a.scales};
+    const int rows = a.cache.page_size < kTile ? a.cache.page_size : kTile;
+    CUtensorMap mk, mv;
+    if (!encode_code_pages(&mk, a.cache, a.cache.k, rows) || !encode_code_pages(&mv, a.cache, a.cache.v, rows)) return ULYSSES_ERR_CUDA;
     auto kern = paged_chunk8_kernel<D>;
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ULYSSES_ERR_CUDA;
-    return launch_chained(kern, dim3(unsigned(p.parts.ctas)), kChunkThreads, C::SMEM_BYTES, stream, mq, p, pool, int(behind_decode))
+    return launch_chained(kern, dim3(unsigned(p.parts.ctas)), kChunkThreads, C::SMEM_BYTES, stream, mq, mk, mv, p, a.scales,
+                          __builtin_ctz(unsigned(rows)), int(behind_decode))
                ? ULYSSES_OK : ULYSSES_ERR_CUDA;
 }
 

@@ -425,6 +425,13 @@ bool encode_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* bas
 // The same of an 8-bit pool's codes, (d elements, token, head, page), swizzled by the row's length.
 bool encode_code_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void* base, int rows);
 
+// Byte offset of 16-byte unit u of key r in a tile of D-byte rows: the 128-byte swizzle for d = 128, the 64-byte one for
+// d = 64. Page copies are whole multiples of the swizzle's period, so the tile is one block whatever the page size.
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int r, int u) {
+    return D == 128 ? uint32_t(r) * 128u + (uint32_t(u ^ (r & 7)) << 4) : uint32_t(r) * 64u + (uint32_t(u ^ ((r >> 1) & 3)) << 4);
+}
+
 // Requests of few rows (paged_decode.cu), and the others (paged_chunk.cu): where their pieces lie in a
 // workspace on a device of `sms` SMs (`bytes` of it, whatever the device), and their launches.
 int paged_decode_rows();

@@ -76,13 +76,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return reinterpret_cast<const uint32_t&>(v);
 }
 
-// Byte offset of 16-byte unit u of key r in a tile of D-byte rows: the 128-byte swizzle for d = 128, the 64-byte one for
-// d = 64. Page copies are whole multiples of the swizzle's period, so the tile is one block whatever the page size.
-template <int D>
-__device__ __forceinline__ uint32_t code_offset(int r, int u) {
-    return D == 128 ? uint32_t(r) * 128u + (uint32_t(u ^ (r & 7)) << 4) : uint32_t(r) * 64u + (uint32_t(u ^ ((r >> 1) & 3)) << 4);
-}
-
 // The exponent of a row's largest magnitude, from the bits of |q| (bf16 pairs) of the lane's part, over the four lanes of
 // the row. At least -100, so that 2^(14 - e) is finite; 128 with an infinity.
 __device__ __forceinline__ int row_exponent(uint32_t top) {
