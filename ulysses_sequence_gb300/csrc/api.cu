@@ -103,12 +103,13 @@ thread_local MapSlot t_maps[64];
 
 bool encode_memo(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base, const cuuint64_t* dims,
                  const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* estr,
-                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     if (rank == 0 || rank > 5) return false;
     MapKey k;
     std::memset(&k, 0, sizeof(k));
     k.dtype = uint64_t(dtype);
-    k.rank = rank | uint64_t(swizzle) << 32;
+    k.rank = rank | uint64_t(swizzle) << 32 | uint64_t(promotion) << 48;
     k.base = reinterpret_cast<uintptr_t>(base);
     for (uint32_t i = 0; i < rank; ++i) {
         k.dims[i] = dims[i];
@@ -130,7 +131,7 @@ bool encode_memo(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, con
         if (!load_encode_fn()) return false;
     }
     if (g_encode(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                 swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 swizzle, promotion,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     sl.key = k;
@@ -143,8 +144,8 @@ bool encode_memo(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, con
 
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
                        const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                       const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle) {
-    return encode_memo(map, dtype, rank, base, dims, strides, box, elem_strides, swizzle);
+                       const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+    return encode_memo(map, dtype, rank, base, dims, strides, box, elem_strides, swizzle, promotion);
 }
 
 bool encode_qkv_map(CUtensorMap* map, const void* base, const ulysses_shape_t& s, int layout, int box_rows,

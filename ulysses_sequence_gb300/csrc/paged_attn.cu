@@ -34,7 +34,8 @@ bool encode_code_pages(CUtensorMap* map, const ulysses_kv_cache_t& c, const void
     cuuint32_t box[5] = {cuuint32_t(c.d_h), cuuint32_t(rows), 1, 1, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, estr,
-                             c.d_h == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                             c.d_h == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                             c.d_h == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
 }
 
 // Behind the decode kernel alone one block joins a whole unit, of up to a dozen pieces and more; with the

@@ -41,7 +41,7 @@ struct RopeSide {          // q or k
     const void* w;            // nullptr: no norm
     float* dw;
     int64_t x_stride, out_stride;  // elements between rows
-    int heads, chunks;
+    int heads, chunks, passes;  // passes of a chunk
 };
 
 struct RopeParams {
@@ -109,28 +109,30 @@ __device__ __forceinline__ void rope_angles(const RopeParams& p, const uint64_t*
     }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+// A lane's 16 elements as pairs of neighbours, the first piece's four and the second's: two fp32 operations to an
+// instruction.
+__device__ __forceinline__ void unpack8(const uint4& v, float2* f) {
     const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(r[i] << 16);
-        f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+    return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
 }
 
-// v: the lane's 16 elements, first piece then second
 template <bool INTER>
-__device__ __forceinline__ void rope_turn(float* v, const float* c, const float* s) {
+__device__ __forceinline__ void rope_turn(float2* v, const float* c, const float* s) {
+    if (INTER) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float& a = INTER ? v[2 * i] : v[i];
-        float& b = INTER ? v[2 * i + 1] : v[8 + i];
-        const float a0 = a, b0 = b;
-        a = a0 * c[i] - b0 * s[i];
-        b = b0 * c[i] + a0 * s[i];
+        for (int i = 0; i < 8; ++i)  // v[i] = (a, b)
+            v[i] = fma2(v[i], make_float2(c[i], c[i]), mul2(make_float2(v[i].y, v[i].x), make_float2(-s[i], s[i])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // a of two pairs in v[i], b in v[4 + i]
+            const float2 a = v[i], b = v[4 + i], cc = make_float2(c[2 * i], c[2 * i + 1]), ss = make_float2(s[2 * i], s[2 * i + 1]);
+            v[i] = fma2(a, cc, mul2(b, make_float2(-ss.x, -ss.y)));
+            v[4 + i] = fma2(b, cc, mul2(a, ss));
+        }
     }
 }
 
@@ -141,15 +143,24 @@ __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void load_weights(const void* w, int wide, int at, float* out) {
+// 1 / sqrt(mean x^2 + eps) of the lane's head
+template <int D>
+__device__ __forceinline__ float inverse_rms(const float2* x, float eps) {
+    float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) ss = fma2(x[i], x[i], ss);
+    return rsqrtf(head_sum<RopeCfg<D>::LPH>(ss.x + ss.y) * (1.0f / D) + eps);
+}
+
+__device__ __forceinline__ void load_weights(const void* w, int wide, int at, float2* out) {
     if (wide) {
         const float* f = static_cast<const float*>(w) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = f[i];
+        for (int i = 0; i < 4; ++i) out[i] = make_float2(f[2 * i], f[2 * i + 1]);
     } else {
         const __nv_bfloat16* f = static_cast<const __nv_bfloat16*>(w) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = __bfloat162float(f[i]);
+        for (int i = 0; i < 4; ++i) out[i] = make_float2(__bfloat162float(f[2 * i]), __bfloat162float(f[2 * i + 1]));
     }
 }
 
@@ -176,59 +187,66 @@ __device__ __forceinline__ void load_turns(const RopeParams& p, uint64_t* f) {
     }
 }
 
-// U passes of heads a row and warp; all their loads go out together, before the angles are known.
+// A warp goes through its chunk's passes U at a time; U passes' loads go out together, the first before the angles are known.
 template <int D, bool NORM, bool INTER, int U>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_fwd_kernel(const RopeParams p) {
     using C = RopeCfg<D>;
     const bool key = int(blockIdx.y) >= p.side[0].chunks;
     const RopeSide& t = p.side[key ? 1 : 0];
-    const int first = (int(blockIdx.y) - (key ? p.side[0].chunks : 0)) * U * C::HPW;
+    const int begin = (int(blockIdx.y) - (key ? p.side[0].chunks : 0)) * t.passes * C::HPW;
+    const int end = min(t.heads, begin + t.passes * C::HPW);
     const RopeLane<D, INTER> at(p.rot);
     grid_wait();
     grid_release();
     uint64_t f[C::PPL];
     load_turns<D>(p, f);
-    float w[16];
+    float2 w[8];
     if (NORM) {
         load_weights(t.w, p.wide, at.ea, w);
-        load_weights(t.w, p.wide, at.eb, w + 8);
+        load_weights(t.w, p.wide, at.eb, w + 4);
     }
     for (int64_t m = int64_t(blockIdx.x) * kRopeWarps + warp_id(); m < p.rows; m += int64_t(gridDim.x) * kRopeWarps) {
+        const __nv_bfloat16* src = t.x + m * t.x_stride;
+        __nv_bfloat16* dst = t.out + m * t.out_stride;
         uint4 v[U][2];
+        auto load = [&](int first) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = first + u * C::HPW + at.g;
-            v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
-            if (h < t.heads) {
-                const __nv_bfloat16* src = t.x + m * t.x_stride + h * D;
-                v[u][0] = *reinterpret_cast<const uint4*>(src + at.ea);
-                v[u][1] = *reinterpret_cast<const uint4*>(src + at.eb);
+            for (int u = 0; u < U; ++u) {
+                const int h = first + u * C::HPW + at.g;
+                v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+                if (h < end) {
+                    v[u][0] = *reinterpret_cast<const uint4*>(src + h * D + at.ea);
+                    v[u][1] = *reinterpret_cast<const uint4*>(src + h * D + at.eb);
+                }
             }
-        }
+        };
+        load(begin);
         int64_t pos;
         if (!rope_position(p, int(m), pos)) continue;
         float c[8], s[8];
         rope_angles<D>(p, f, pos, c, s);
+        for (int first = begin;;) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = first + u * C::HPW + at.g;
-            float x[16];
-            unpack8(v[u][0], x);
-            unpack8(v[u][1], x + 8);
-            if (NORM) {
-                float ss = 0.f;
+            for (int u = 0; u < U; ++u) {
+                const int h = first + u * C::HPW + at.g;
+                float2 x[8];
+                unpack8(v[u][0], x);
+                unpack8(v[u][1], x + 4);
+                if (NORM) {
+                    const float r = inverse_rms<D>(x, p.eps);
+                    const float2 rr = make_float2(r, r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
-                const float r = rsqrtf(head_sum<C::LPH>(ss) * (1.0f / D) + p.eps);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+                    for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], rr), w[i]);
+                }
+                if (at.turned) rope_turn<INTER>(x, c, s);
+                if (h < end) {
+                    *reinterpret_cast<uint4*>(dst + h * D + at.ea) = pack8(x);
+                    *reinterpret_cast<uint4*>(dst + h * D + at.eb) = pack8(x + 4);
+                }
             }
-            if (at.turned) rope_turn<INTER>(x, c, s);
-            if (h < t.heads) {
-                __nv_bfloat16* dst = t.out + m * t.out_stride + h * D;
-                *reinterpret_cast<uint4*>(dst + at.ea) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + at.eb) = pack8(x + 8);
-            }
+            first += U * C::HPW;
+            if (first >= end) break;
+            load(first);
         }
     }
 }
@@ -245,11 +263,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeP
     grid_release();
     uint64_t f[C::PPL];
     load_turns<D>(p, f);
-    float w[16], dw[16];
+    float2 w[8], dw[8];
     load_weights(t.w, p.wide, at.ea, w);
-    load_weights(t.w, p.wide, at.eb, w + 8);
+    load_weights(t.w, p.wide, at.eb, w + 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+    for (int i = 0; i < 8; ++i) dw[i] = make_float2(0.f, 0.f);
     for (int64_t m = int64_t(blockIdx.x) * kRopeWarps + warp_id(); m < p.rows; m += int64_t(gridDim.x) * kRopeWarps) {
         uint4 v[U][2], y[U][2];
 #pragma unroll
@@ -271,31 +289,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeP
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = first + u * C::HPW + at.g;
-            float x[16], g[16];
+            float2 x[8], g[8];
             unpack8(v[u][0], x);
-            unpack8(v[u][1], x + 8);
+            unpack8(v[u][1], x + 4);
             unpack8(y[u][0], g);
-            unpack8(y[u][1], g + 8);
+            unpack8(y[u][1], g + 4);
             if (at.turned) rope_turn<INTER>(g, c, s);
-            float ss = 0.f;
+            const float r = inverse_rms<D>(x, p.eps);
+            const float2 rr = make_float2(r, r);
+            float2 gx = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
-            const float r = rsqrtf(head_sum<C::LPH>(ss) * (1.0f / D) + p.eps);
-            float gx = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] *= r;
-                dw[i] = fmaf(g[i], x[i], dw[i]);  // a head that is not there adds 0 * 0
-                g[i] *= w[i];
-                gx = fmaf(g[i], x[i], gx);
+            for (int i = 0; i < 8; ++i) {
+                x[i] = mul2(x[i], rr);
+                dw[i] = fma2(g[i], x[i], dw[i]);  // a head that is not there adds 0 * 0
+                g[i] = mul2(g[i], w[i]);
+                gx = fma2(g[i], x[i], gx);
             }
-            const float mean = head_sum<C::LPH>(gx) * (1.0f / D);
+            const float mean = head_sum<C::LPH>(gx.x + gx.y) * (-1.0f / D);
+            const float2 mm = make_float2(mean, mean);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = r * fmaf(-mean, x[i], g[i]);
+            for (int i = 0; i < 8; ++i) x[i] = mul2(rr, fma2(mm, x[i], g[i]));
             if (h < t.heads) {
                 __nv_bfloat16* dst = t.out + m * t.out_stride + h * D;
                 *reinterpret_cast<uint4*>(dst + at.ea) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + at.eb) = pack8(x + 8);
+                *reinterpret_cast<uint4*>(dst + at.eb) = pack8(x + 4);
             }
         }
     }
@@ -303,9 +320,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeP
     __shared__ float sum[kRopeWarps][D];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+        float d = i & 1 ? dw[i / 2].y : dw[i / 2].x;
 #pragma unroll
-        for (int o = C::LPH; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-        if (at.g == 0) sum[warp_id()][(i < 8 ? at.ea : at.eb) + i % 8] = dw[i];
+        for (int o = C::LPH; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (at.g == 0) sum[warp_id()][(i < 8 ? at.ea : at.eb) + i % 8] = d;
     }
     __syncthreads();
     if (threadIdx.x < D) {
@@ -357,14 +375,19 @@ int launch_fwd_t(const RopeParams& p, bool inter, dim3 grid, cudaStream_t stream
 template <int D>
 int launch_fwd_d(RopeParams& p, bool inter, cudaStream_t stream) {
     const bool norm = p.side[0].w != nullptr;
-    // few rows: one pass to a warp, for as many warps as there are
-    const int total = passes(p.side[0].heads, D) + passes(p.side[1].heads, D);
-    const bool few = int64_t(p.rows) * total <= int64_t(device_sm_count()) * 32;
-    const int U = few ? 1 : 2;
-    for (RopeSide& t : p.side) t.chunks = chunks_of(t.heads, D, U);
+    // A warp takes all heads of q or k of its row, two passes at a time, and computes the row's angles once for them; where that
+    // leaves the GPU's warps without work, parts of them, down to one pass (64 rows of 32 + 8 heads of 128: 2.0 us; with all
+    // heads to a warp 4.1 us; 32768 rows with norms: 106 us, with one pass to a warp 177 us).
+    const int most = std::max(passes(p.side[0].heads, D), passes(p.side[1].heads, D)), warps = device_sm_count() * 24;
+    int per = 1;
+    while (per < most && int64_t(p.rows) * (most / (2 * per) + 1) >= warps) per *= 2;
+    for (RopeSide& t : p.side) {
+        t.passes = per;
+        t.chunks = chunks_of(t.heads, D, per);
+    }
     const int64_t blocks = (int64_t(p.rows) + kRopeWarps - 1) / kRopeWarps;
     const dim3 grid(unsigned(blocks), unsigned(p.side[0].chunks + p.side[1].chunks));
-    if (few) return norm ? launch_fwd_t<D, true, 1>(p, inter, grid, stream) : launch_fwd_t<D, false, 1>(p, inter, grid, stream);
+    if (per == 1) return norm ? launch_fwd_t<D, true, 1>(p, inter, grid, stream) : launch_fwd_t<D, false, 1>(p, inter, grid, stream);
     return norm ? launch_fwd_t<D, true, 2>(p, inter, grid, stream) : launch_fwd_t<D, false, 2>(p, inter, grid, stream);
 }
 

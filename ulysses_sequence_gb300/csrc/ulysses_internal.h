@@ -35,11 +35,12 @@ inline KvInfo kv_info(const ulysses_shape_t& s) {
     return k;
 }
 
-// cuTensorMapEncodeTiled (looked up at run time) with the 128-byte swizzle (or the one given), 256-byte
-// L2 promotion and zero fill out of bounds.
+// cuTensorMapEncodeTiled (looked up at run time) with the 128-byte swizzle and 256-byte L2 promotion (or
+// those given) and zero fill out of bounds.
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
                        const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                       const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+                       const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                       CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Encodes a 5-D bf16 tensor map over (d, head, row, batch, unit) with a box of
 // (64, 1, box_rows, 1, 1), 128-byte swizzle and zero fill out of bounds, for a tensor with
