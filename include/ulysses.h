@@ -289,7 +289,8 @@ typedef struct {
  * not used). The norm and rotation are computed in fp32 and rounded once. q_out may be q and k_out may be k
  * (in place).
  * TOKEN_SHARDED needs L % P == 0, but not H % P == 0 (the shards of the Ulysses-ring hybrid).
- * Supported: d_h in {64, 128}, fewer than 2^31 rows (B * L, head-sharded P * B * L). Tensors 16-byte aligned. */
+ * Supported: d_h in {64, 128}, fewer than 2^31 rows (B * L, head-sharded P * B * L), rows of up to 2^23
+ * elements. Tensors 16-byte aligned. */
 int ulysses_qk_rope_fwd(ulysses_shape_t shape, int io_layout, const ulysses_rope_t *rope, int64_t pos0, const void *q,
                         const void *k, const void *w_q, const void *w_k, int w_fp32, float eps, void *q_out, void *k_out,
                         void *stream);
@@ -430,7 +431,8 @@ typedef struct {
  *   - code = x / scale to the nearest (ties to even); magnitudes past 448 * 2^119 and infinities become 448, NaN stays
  *     NaN and does not count for amax.
  * Tokens of one block must be consecutive rows of one call, as ulysses_page_plan places them: rows of one
- * block that are separated by another block's give undefined codes and scales in it. Tokens whose slot lies outside the pool
+ * block that are separated by another block's give undefined codes and scales in it. Slots should be distinct: where two
+ * rows name the same one, each 8-byte piece of it holds one or the other. Tokens whose slot lies outside the pool
  * are skipped. d_h: 64 or 128. */
 int ulysses_kv_append8(const ulysses_kv_cache8_t *cache, int T, const void *k, int64_t k_stride, const void *v,
                        int64_t v_stride, const int32_t *slot_map, void *stream);

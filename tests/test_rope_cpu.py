@@ -116,7 +116,7 @@ def test_rows_misaligned(kw):
     assert rows(**kw) == U.ERR_MISALIGNED
 
 
-@pytest.mark.parametrize("kw", [dict(d=96, r=turn(rot=0)), dict(H=1 << 19, qs=1 << 26, qos=1 << 26), dict(qs=(1 << 31) + 8), dict(kos=1 << 33)])
+@pytest.mark.parametrize("kw", [dict(d=96, r=turn(rot=0)), dict(H=1 << 19, qs=1 << 26, qos=1 << 26), dict(H=(1 << 17) + 1, qs=1 << 24, qos=1 << 24), dict(qs=(1 << 31) + 8), dict(kos=1 << 33)])
 def test_rows_unsupported(kw):
     assert rows(**kw) == U.ERR_UNSUPPORTED
 

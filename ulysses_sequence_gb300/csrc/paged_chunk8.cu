@@ -81,6 +81,21 @@ static_assert(2 * sizeof(ChunkPiece) <= 128, "piece ring");
 constexpr uint32_t kInfoEnd = 0x200;
 constexpr uint32_t kInfoMasked = 0x100;  // some row does not see all of the tile; bits 0-7: pages of 16 keys that exist
 
+// mbar_wait for kernels whose waits are inline: the first one that runs out leaves its role and site in the abort flag, from
+// where the block's end takes it to the error word.
+__device__ __forceinline__ bool chunk8_wait(uint64_t* bar, uint32_t parity, volatile int* flag, uint32_t role, uint32_t site) {
+    const uint32_t a = smem_u32(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(a, parity)) return true;
+        if (*flag) return false;
+    } while (globaltimer_ns() - t0 <= kWaitLimitNs);
+    *flag = int((role << 16) | site);
+    return false;
+}
+
 // 16 codes as bf16 times a power of two, exactly: two pieces of 8.
 __device__ __forceinline__ void widen16(const uint4& c, float scale, uint4& lo, uint4& hi) {
     const uint32_t r[4] = {c.x, c.y, c.z, c.w};
@@ -183,216 +198,216 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Abort ab{abort_flag, p.err, KID_PAGED};
+    volatile int* ab = abort_flag;
 
     // each warpgroup gives or takes its registers at the head of its branch, where the compiler counts them
     if (warp < 4) {
-    regs_dec<kRegsIssue>();
-    if (warp == 0) {
-        // ------------------------------------------------------------------ producer
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-        }
-        if (p.B <= kLaneRequests) paged_share_lanes(p, kChunkMinCost, w);
-        else if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
-        // lane l of the first 16 looks up the page of keys [16 (l % 8), + 16), and the scale of the keys (l < 8) or values
-        // there; the first of a copy's lanes issues it
-        const int my_key = (lane & 7) * 16;
-        const bool copies = lane < 8 && (my_key & ((1 << log_rows) - 1)) == 0;
-        auto lookup = [&](int key0) {
-            const int key = key0 + my_key;
-            const int id = lane < 16 && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
-            return unsigned(id) < unsigned(p.num_pages) ? id : -1;
-        };
-        const uint8_t* scale_of = lane < 8 ? scales.k : scales.v;
-        auto scale = [&](int id, int key0) {
-            if (id < 0) return 127;
-            const int token = (key0 + my_key) & ((1 << p.page_shift) - 1);
-            const int64_t at = (int64_t(id) << (p.page_shift - scales.block_shift)) + (token >> scales.block_shift);
-            return int(scale_of[at * p.Hkv + w.head]);
-        };
-        PagedMeta meta{0, 0, 0, 0};
-        int n = 0, nc = 0, nq = 0, piece = 0;  // tiles, stages of codes, copies of queries and pieces so far
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_LOAD, site));
-        };
-        auto room = [&](uint32_t site) { return nc < C::NSC || wait(c_empty + nc % C::NSC, ((nc / C::NSC) - 1) & 1, site); };
-        auto copy = [&](const CUtensorMap* map, int id, int key0) {
-            const int st = nc++ % C::NSC;
-            if (lane == 0) mbar_arrive_expect_tx(c_full + st, C::CODE_BYTES);
-            __syncwarp();
-            // a page that does not exist is copied from behind the pool: zeros
-            if (copies)
-                tma_load_5d(sC + st * C::CODE_BYTES + my_key * D, map, c_full + st, 0, (key0 + my_key) & ((1 << p.page_shift) - 1),
-                            w.head, id >= 0 ? id : p.num_pages, 0);
-        };
-        while (ok && w.left > 0) {
-            // the next piece: what this CTA does of the walk's unit
-            int off, tiles;
-            w.take(off, tiles);
-            if (tiles == 0) {
-                if (w.left > 0) w.next_unit(p);
-                continue;
-            }
-            const int tokens = w.t1 - w.t0, row0 = w.s.start + w.t0, pos = w.s.base + w.t0;
-            const int key_first = (w.first + off) * kTile;
-            int slot = -1;
-            if (piece == 0 && off > 0) {
-                slot = 2 * cta;
-            } else if (off + tiles < w.count) {
-                slot = 2 * cta + 1;
-                meta = PagedMeta{w.pieces(cta), w.head, row0, tokens * p.G};
-            }
-            if (piece >= 2 && !(ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 1))) break;
+        regs_dec<kRegsIssue>();
+        if (warp == 0) {
+            // ------------------------------------------------------------------ producer
             if (lane == 0) {
-                pieces[piece & 1] = ChunkPiece{tiles, key_first, w.s.kv, pos, row0, tokens, w.head, slot};
-                mbar_arrive(piece_full + (piece & 1));
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
             }
-            int id = lookup(key_first);
-            int byte = scale(id, key_first);
-            for (int i = 0; i < tiles; ++i) {
-                const int key0 = key_first + i * kTile;
-                const int id_next = i + 1 < tiles ? lookup(key0 + kTile) : -1;
-                if (!(ok = room(2))) break;
-                const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0) & 0xffu;
-                ChunkTile* t = tile_info(n);
-                if (lane < 16) (lane < 8 ? t->k : t->v)[lane & 7] = __uint_as_float(uint32_t(byte) << 23);
-                if (lane == 0) {
-                    // clear: every row of the unit sees every key of the tile
-                    const bool clear = valid == 0xff && key0 + kTile <= w.s.kv &&
-                                       (!p.causal || (key0 + kTile <= pos + 1 && (p.window == 0 || key0 > pos + tokens - 1 - p.window)));
-                    t->what = valid | (clear ? 0u : kInfoMasked);
-                    t->limit = w.s.kv - key0;
-                }
+            if (p.B <= kLaneRequests) paged_share_lanes(p, kChunkMinCost, w);
+            else if (p.B <= kFewRequests) paged_share_warp(p, kChunkMinCost, costs, w);
+            // lane l of the first 16 looks up the page of keys [16 (l % 8), + 16), and the scale of the keys (l < 8) or values
+            // there; the first of a copy's lanes issues it
+            const int my_key = (lane & 7) * 16;
+            const bool copies = lane < 8 && (my_key & ((1 << log_rows) - 1)) == 0;
+            auto lookup = [&](int key0) {
+                const int key = key0 + my_key;
+                const int id = lane < 16 && key < w.s.kv ? p.table[w.i * p.table_stride + (key >> p.page_shift)] : -1;
+                return unsigned(id) < unsigned(p.num_pages) ? id : -1;
+            };
+            const uint8_t* scale_of = lane < 8 ? scales.k : scales.v;
+            auto scale = [&](int id, int key0) {
+                if (id < 0) return 127;
+                const int token = (key0 + my_key) & ((1 << p.page_shift) - 1);
+                const int64_t at = (int64_t(id) << (p.page_shift - scales.block_shift)) + (token >> scales.block_shift);
+                return int(scale_of[at * p.Hkv + w.head]);
+            };
+            PagedMeta meta{0, 0, 0, 0};
+            int n = 0, nc = 0, nq = 0, piece = 0;  // tiles, stages of codes, copies of queries and pieces so far
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+                return __all_sync(0xffffffffu, chunk8_wait(bar, parity, ab, ROLE_LOAD, site));
+            };
+            auto room = [&](uint32_t site) { return nc < C::NSC || wait(c_empty + nc % C::NSC, ((nc / C::NSC) - 1) & 1, site); };
+            auto copy = [&](const CUtensorMap* map, int id, int key0) {
+                const int st = nc++ % C::NSC;
+                if (lane == 0) mbar_arrive_expect_tx(c_full + st, C::CODE_BYTES);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(info_full + n % C::RING);
-                ++n;
-                copy(&tm_k, id, key0);
-                if (i == 0) {
-                    // the unit's queries, once the previous piece's last scores are computed
-                    if (piece >= 1 && !(ok = wait(q_empty, (piece - 1) & 1, 3))) break;
-                    const int n_t = tokens > TOK ? 2 : 1;
+                // a page that does not exist is copied from behind the pool: zeros
+                if (copies)
+                    tma_load_5d(sC + st * C::CODE_BYTES + my_key * D, map, c_full + st, 0, (key0 + my_key) & ((1 << p.page_shift) - 1),
+                                w.head, id >= 0 ? id : p.num_pages, 0);
+            };
+            while (ok && w.left > 0) {
+                // the next piece: what this CTA does of the walk's unit
+                int off, tiles;
+                w.take(off, tiles);
+                if (tiles == 0) {
+                    if (w.left > 0) w.next_unit(p);
+                    continue;
+                }
+                const int tokens = w.t1 - w.t0, row0 = w.s.start + w.t0, pos = w.s.base + w.t0;
+                const int key_first = (w.first + off) * kTile;
+                int slot = -1;
+                if (piece == 0 && off > 0) {
+                    slot = 2 * cta;
+                } else if (off + tiles < w.count) {
+                    slot = 2 * cta + 1;
+                    meta = PagedMeta{w.pieces(cta), w.head, row0, tokens * p.G};
+                }
+                if (piece >= 2 && !(ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 1))) break;
+                if (lane == 0) {
+                    pieces[piece & 1] = ChunkPiece{tiles, key_first, w.s.kv, pos, row0, tokens, w.head, slot};
+                    mbar_arrive(piece_full + (piece & 1));
+                }
+                int id = lookup(key_first);
+                int byte = scale(id, key_first);
+                for (int i = 0; i < tiles; ++i) {
+                    const int key0 = key_first + i * kTile;
+                    const int id_next = i + 1 < tiles ? lookup(key0 + kTile) : -1;
+                    if (!(ok = room(2))) break;
+                    const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0) & 0xffu;
+                    ChunkTile* t = tile_info(n);
+                    if (lane < 16) (lane < 8 ? t->k : t->v)[lane & 7] = __uint_as_float(uint32_t(byte) << 23);
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full, uint32_t(n_t * (D / 64)) * uint32_t(TOK * p.G) * 128u);
-                        for (int t = 0; t < n_t; ++t)
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load_5d(sQ + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_q, q_full, 0, w.head * p.G,
-                                            row0 + t * TOK, c, 0);
+                        // clear: every row of the unit sees every key of the tile
+                        const bool clear = valid == 0xff && key0 + kTile <= w.s.kv &&
+                                           (!p.causal || (key0 + kTile <= pos + 1 && (p.window == 0 || key0 > pos + tokens - 1 - p.window)));
+                        t->what = valid | (clear ? 0u : kInfoMasked);
+                        t->limit = w.s.kv - key0;
                     }
                     __syncwarp();
-                    ++nq;
-                }
-                if (!(ok = room(4))) break;
-                copy(&tm_v, id, key0);
-                id = id_next;
-                byte = scale(id, key0 + kTile);
-            }
-            if (!ok) break;
-            ++piece;
-            if (w.left > 0) w.next_unit(p);
-        }
-        if (ok && (ok = room(6)) && lane == 0) {
-            tile_info(n)->what = kInfoEnd;
-            mbar_arrive(info_full + n % C::RING);
-        }
-        if (ok && (piece < 2 || (ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 5))) && lane == 0) {
-            pieces[piece & 1].tiles = 0;
-            mbar_arrive(piece_full + (piece & 1));
-        }
-        if (lane == 0) {
-            p.parts.meta[cta] = meta;
-            // every copy lands before the CTA can exit, also where another role has given up since
-            ring_drain<1>(q_full, nq);
-            ring_drain<C::NSC>(c_full, nc);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
-        {
-            const uint32_t one = elect_one();
-            auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_MMA, site));
-            };
-            constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-            constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
-            const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
-            bool ok = true;
-            int j = 0;                          // key tiles so far
-            int s0 = 0, s1 = 0, c0 = 0, c1 = 0; // S_t and PV_t so far
-            int bs = 0, bp = 0;                 // AHEAD: S buffer of the next S and of the next PV
-            auto issue_s = [&](int t, int sk, int& c) {  // S_t = Q_t K^T
-                const uint64_t dq = sdesc_sw128(aQ + t * C::TILE_BYTES, 16, 1024);
-                const uint64_t dk = sdesc_sw128(aK + sk * C::TILE_BYTES, 16, 1024);
-                const uint32_t col = kTile * (C::AHEAD ? bs : t);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k >> 2) * C::CHUNK_BYTES + (k & 3) * 32;
-                    umma_ss_one(one, col, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
-                }
-                umma_commit_one(one, tile_bar(s_full, t, c++));
-                bs = next_buffer(bs, 1);
-            };
-            auto issue_pv = [&](int t, int sv, bool first, bool last) {  // O_t (+)= P_t V
-                const uint64_t dv = sdesc_sw128(aV + sv * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
-                const uint32_t col = kTile * (C::AHEAD ? bp : t);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)  // 16 keys = 8 TMEM columns of P per step
-                    umma_ts_one(one, C::COL_O + D * t, col + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
-                if (C::AHEAD || last) umma_commit_one(one, o_done + t);
-                bp = next_buffer(bp, 1);
-            };
-            for (int piece = 0; ok; ++piece) {
-                if (!(ok = wait(piece_full + (piece & 1), (piece >> 1) & 1, 1))) break;
-                const int n = pieces[piece & 1].tiles;
-                const bool two = pieces[piece & 1].tokens > TOK;
-                if (n == 0) break;
-                __syncwarp();
-                if (one) mbar_arrive(piece_empty + (piece & 1));
-                if (!(ok = wait(q_full, piece & 1, 2))) break;
-                if (!(ok = wait(k_full + j % NSK, (j / NSK) & 1, 3))) break;
-                tc_fence_after();
-                issue_s(0, j % NSK, s0);
-                if (two) issue_s(1, j % NSK, s1);
-                umma_commit_one(one, k_empty + j % NSK);
-                if (n == 1) umma_commit_one(one, q_empty);
-                for (int i = 0; i < n; ++i, ++j) {
-                    const bool next = i + 1 < n;
-                    const int sv = j % NSV, sk = (j + 1) % NSK;
-                    if (C::AHEAD && next) {
-                        if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
-                        tc_fence_after();
-                        issue_s(0, sk, s0);
+                    if (lane == 0) mbar_arrive(info_full + n % C::RING);
+                    ++n;
+                    copy(&tm_k, id, key0);
+                    if (i == 0) {
+                        // the unit's queries, once the previous piece's last scores are computed
+                        if (piece >= 1 && !(ok = wait(q_empty, (piece - 1) & 1, 3))) break;
+                        const int n_t = tokens > TOK ? 2 : 1;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_full, uint32_t(n_t * (D / 64)) * uint32_t(TOK * p.G) * 128u);
+                            for (int t = 0; t < n_t; ++t)
+                                for (int c = 0; c < D / 64; ++c)
+                                    tma_load_5d(sQ + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_q, q_full, 0, w.head * p.G,
+                                                row0 + t * TOK, c, 0);
+                        }
+                        __syncwarp();
+                        ++nq;
                     }
-                    if (!(ok = wait(v_full + sv, (j / NSV) & 1, 4))) break;
-                    if (!(ok = wait(tile_bar(p_full, 0, c0), tile_phase(c0), 5))) break;
-                    ++c0;
+                    if (!(ok = room(4))) break;
+                    copy(&tm_v, id, key0);
+                    id = id_next;
+                    byte = scale(id, key0 + kTile);
+                }
+                if (!ok) break;
+                ++piece;
+                if (w.left > 0) w.next_unit(p);
+            }
+            if (ok && (ok = room(6)) && lane == 0) {
+                tile_info(n)->what = kInfoEnd;
+                mbar_arrive(info_full + n % C::RING);
+            }
+            if (ok && (piece < 2 || (ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 5))) && lane == 0) {
+                pieces[piece & 1].tiles = 0;
+                mbar_arrive(piece_full + (piece & 1));
+            }
+            if (lane == 0) {
+                p.parts.meta[cta] = meta;
+                // every copy lands before the CTA can exit, also where another role has given up since
+                ring_drain<1>(q_full, nq);
+                ring_drain<C::NSC>(c_full, nc);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------------ MMA issuer
+            {
+                const uint32_t one = elect_one();
+                auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+                    return __all_sync(0xffffffffu, chunk8_wait(bar, parity, ab, ROLE_MMA, site));
+                };
+                constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+                constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+                const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+                bool ok = true;
+                int j = 0;                          // key tiles so far
+                int s0 = 0, s1 = 0, c0 = 0, c1 = 0; // S_t and PV_t so far
+                int bs = 0, bp = 0;                 // AHEAD: S buffer of the next S and of the next PV
+                auto issue_s = [&](int t, int sk, int& c) {  // S_t = Q_t K^T
+                    const uint64_t dq = sdesc_sw128(aQ + t * C::TILE_BYTES, 16, 1024);
+                    const uint64_t dk = sdesc_sw128(aK + sk * C::TILE_BYTES, 16, 1024);
+                    const uint32_t col = kTile * (C::AHEAD ? bs : t);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = (k >> 2) * C::CHUNK_BYTES + (k & 3) * 32;
+                        umma_ss_one(one, col, sdesc_add(dq, o), sdesc_add(dk, o), idS, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit_one(one, tile_bar(s_full, t, c++));
+                    bs = next_buffer(bs, 1);
+                };
+                auto issue_pv = [&](int t, int sv, bool first, bool last) {  // O_t (+)= P_t V
+                    const uint64_t dv = sdesc_sw128(aV + sv * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
+                    const uint32_t col = kTile * (C::AHEAD ? bp : t);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)  // 16 keys = 8 TMEM columns of P per step
+                        umma_ts_one(one, C::COL_O + D * t, col + k * 8, sdesc_add(dv, k * 2048), idO, (!first || k > 0) ? 1u : 0u);
+                    if (C::AHEAD || last) umma_commit_one(one, o_done + t);
+                    bp = next_buffer(bp, 1);
+                };
+                for (int piece = 0; ok; ++piece) {
+                    if (!(ok = wait(piece_full + (piece & 1), (piece >> 1) & 1, 1))) break;
+                    const int n = pieces[piece & 1].tiles;
+                    const bool two = pieces[piece & 1].tokens > TOK;
+                    if (n == 0) break;
+                    __syncwarp();
+                    if (one) mbar_arrive(piece_empty + (piece & 1));
+                    if (!(ok = wait(q_full, piece & 1, 2))) break;
+                    if (!(ok = wait(k_full + j % NSK, (j / NSK) & 1, 3))) break;
                     tc_fence_after();
-                    issue_pv(0, sv, i == 0, !next);
-                    if (!C::AHEAD && next) {
-                        if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
+                    issue_s(0, j % NSK, s0);
+                    if (two) issue_s(1, j % NSK, s1);
+                    umma_commit_one(one, k_empty + j % NSK);
+                    if (n == 1) umma_commit_one(one, q_empty);
+                    for (int i = 0; i < n; ++i, ++j) {
+                        const bool next = i + 1 < n;
+                        const int sv = j % NSV, sk = (j + 1) % NSK;
+                        if (C::AHEAD && next) {
+                            if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
+                            tc_fence_after();
+                            issue_s(0, sk, s0);
+                        }
+                        if (!(ok = wait(v_full + sv, (j / NSV) & 1, 4))) break;
+                        if (!(ok = wait(tile_bar(p_full, 0, c0), tile_phase(c0), 5))) break;
+                        ++c0;
                         tc_fence_after();
-                        issue_s(0, sk, s0);
+                        issue_pv(0, sv, i == 0, !next);
+                        if (!C::AHEAD && next) {
+                            if (!(ok = wait(k_full + sk, ((j + 1) / NSK) & 1, 6))) break;
+                            tc_fence_after();
+                            issue_s(0, sk, s0);
+                        }
+                        if (two) {
+                            if (C::AHEAD && next) issue_s(1, sk, s1);
+                            if (!(ok = wait(tile_bar(p_full, 1, c1), tile_phase(c1), 7))) break;
+                            ++c1;
+                            tc_fence_after();
+                            issue_pv(1, sv, i == 0, !next);
+                            if (!C::AHEAD && next) issue_s(1, sk, s1);
+                        }
+                        if (next) umma_commit_one(one, k_empty + sk);
+                        if (i + 2 == n) umma_commit_one(one, q_empty);  // the piece's last scores are under way
+                        umma_commit_one(one, v_empty + sv);
                     }
-                    if (two) {
-                        if (C::AHEAD && next) issue_s(1, sk, s1);
-                        if (!(ok = wait(tile_bar(p_full, 1, c1), tile_phase(c1), 7))) break;
-                        ++c1;
-                        tc_fence_after();
-                        issue_pv(1, sv, i == 0, !next);
-                        if (!C::AHEAD && next) issue_s(1, sk, s1);
-                    }
-                    if (next) umma_commit_one(one, k_empty + sk);
-                    if (i + 2 == n) umma_commit_one(one, q_empty);  // the piece's last scores are under way
-                    umma_commit_one(one, v_empty + sv);
                 }
+                // every product is over before the tensor memory is freed, also where a softmax warp has given up since
+                umma_commit_one(one, drain);
+                mbar_drain(drain, 0);
             }
-            // every product is over before the tensor memory is freed, also where a softmax warp has given up since
-            umma_commit_one(one, drain);
-            mbar_drain(drain, 0);
         }
-    }
     } else if (warp >= 12) {
         // ------------------------------------------------------------------ converters
         regs_dec<kRegsConvert>();
@@ -402,30 +417,34 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int my_unit = lane & 3;
         int nc = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, ROLE_LOAD, site));
+            return __all_sync(0xffffffffu, chunk8_wait(bar, parity, ab, ROLE_LOAD, site));
         };
-        // one tile of keys or values: all its codes first, so that no unit's loads stand behind another's stores
-        uint4 x[4][D / 64];
-        auto load = [&] {
-            const uint32_t codes = smem_u32(sC + (nc % C::NSC) * C::CODE_BYTES);
+        // One tile of keys or values, in two halves of four units: the codes of a half first, so that no unit's loads stand
+        // behind another's stores, and a loop, because the roles' code together is more than the instruction cache likes (with
+        // a copy of this for tiles that reach the request's end: 1650 us, one for all without the loop: 1500 us).
+        auto convert = [&](uint8_t* tile, const float* by, int limit) {
+            const uint32_t codes = smem_u32(sC + (nc % C::NSC) * C::CODE_BYTES), out = smem_u32(tile);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                uint4 x[2][D / 64];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)  // 8 rows each
+                for (int g = 0; g < 2; ++g)  // 8 rows each
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) x[g][c] = ld_shared_v4u(codes + code_offset<D>(my_row + 8 * g, 4 * c + my_unit));
-        };
-        auto store = [&](uint8_t* tile, const float* by, int limit) {
+                    for (int c = 0; c < D / 64; ++c)
+                        x[g][c] = ld_shared_v4u(codes + code_offset<D>(my_row + 16 * h + 8 * g, 4 * c + my_unit));
+                const float s = by[cw * 2 + h];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int row = my_row + 8 * g;
-                const uint32_t a = smem_u32(tile) + row * 128, sw = row & 7;
-                const float s = by[cw * 2 + (g >> 1)];
+                for (int g = 0; g < 2; ++g) {
+                    const int row = my_row + 16 * h + 8 * g;
+                    const uint32_t a = out + row * 128, sw = row & 7;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint4 lo, hi;
-                    widen16(x[g][c], s, lo, hi);
-                    if (row >= limit) lo = hi = make_uint4(0, 0, 0, 0);
-                    st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit) ^ sw) << 4), lo.x, lo.y, lo.z, lo.w);
-                    st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit + 1) ^ sw) << 4), hi.x, hi.y, hi.z, hi.w);
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint4 lo, hi;
+                        widen16(x[g][c], s, lo, hi);
+                        if (row >= limit) lo = hi = make_uint4(0, 0, 0, 0);
+                        st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit) ^ sw) << 4), lo.x, lo.y, lo.z, lo.w);
+                        st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit + 1) ^ sw) << 4), hi.x, hi.y, hi.z, hi.w);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -440,10 +459,9 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int value = 0; value < 2 && ok; ++value, ++nc) {
                 const int ns = value ? NSV : NSK, st = j % ns;
                 uint64_t *full = (value ? v_full : k_full) + st, *empty = (value ? v_empty : k_empty) + st;
-                if (!(ok = wait(c_full + nc % C::NSC, (nc / C::NSC) & 1, 12))) break;
-                load();
-                if (!(ok = j < ns || wait(empty, ((j / ns) - 1) & 1, 13))) break;
-                store((value ? sV : sK) + st * C::TILE_BYTES, value ? t->v : t->k, value ? t->limit : kTile);
+                ok = wait(c_full + nc % C::NSC, (nc / C::NSC) & 1, 12) && (j < ns || wait(empty, ((j / ns) - 1) & 1, 13));
+                if (!ok) break;
+                convert((value ? sV : sK) + st * C::TILE_BYTES, value ? t->v : t->k, value ? t->limit : kTile);
                 if (lane == 0) {
                     mbar_arrive(full);
                     mbar_arrive(c_empty + nc % C::NSC);
@@ -465,7 +483,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         int j = 0, cs = 0, units = 0;             // key tiles so far; this tile's S and O so far
         int buffer0 = 0;                          // AHEAD: S buffer of the piece's first scores
         for (int piece = 0; ok; ++piece) {
-            ok = __all_sync(0xffffffffu, mbar_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
+            ok = __all_sync(0xffffffffu, chunk8_wait(piece_full + (piece & 1), (piece >> 1) & 1, ab, ROLE_SOFTMAX, 1));
             if (!ok) break;
             // read again where needed: registers are short in the loop below
             const volatile ChunkPiece& u = pieces[piece & 1];
@@ -494,8 +512,8 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int i = 0; i < tiles; ++i, ++j, key0 += kTile) {
                 const int c = cs++;
                 if (C::AHEAD) tS = tmem + kTile * buffer + lane_off;
-                ok = __all_sync(0xffffffffu, mbar_wait(tile_bar(s_full, t, c), tile_phase(c), ab, ROLE_SOFTMAX, 2) &&
-                                                 mbar_wait(info_full + j % C::RING, (j / C::RING) & 1, ab, ROLE_SOFTMAX, 3));
+                ok = __all_sync(0xffffffffu, chunk8_wait(tile_bar(s_full, t, c), tile_phase(c), ab, ROLE_SOFTMAX, 2) &&
+                                                 chunk8_wait(info_full + j % C::RING, (j / C::RING) & 1, ab, ROLE_SOFTMAX, 3));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t what = tile_info(j)->what;
@@ -547,7 +565,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 l_sum = l_sum * alpha + rs;
                 if (C::AHEAD && i > 0) {
                     // O_t holds still between the product of the key tile before and this one's
-                    ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, units++ & 1, ab, ROLE_SOFTMAX, 5));
+                    ok = __all_sync(0xffffffffu, chunk8_wait(o_done + t, units++ & 1, ab, ROLE_SOFTMAX, 5));
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -570,7 +588,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             if (!ok) break;
             // -------------------------------------------------------------- the piece's rows
-            ok = __all_sync(0xffffffffu, mbar_wait(o_done + t, units++ & 1, ab, ROLE_EPI, 1));
+            ok = __all_sync(0xffffffffu, chunk8_wait(o_done + t, units++ & 1, ab, ROLE_EPI, 1));
             if (!ok) break;
             tc_fence_after();
             const bool any_key = l_sum != 0.f;  // NaN scores stay NaN
@@ -619,6 +637,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     tc_fence_before();
     __syncwarp();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) record_error(p.err, (KID_PAGED << 24) | uint32_t(*abort_flag));
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);

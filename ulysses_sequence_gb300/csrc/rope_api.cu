@@ -6,6 +6,9 @@
 namespace ulysses {
 namespace {
 
+// Elements of a row: the parts of its heads, 512 elements at the least, are rows of a grid.
+constexpr int64_t kRopeMaxRow = 1 << 23;
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int rope_ok(const ulysses_rope_t* rope, int d_h) {
@@ -33,7 +36,7 @@ int place(const ulysses_shape_t& s, int layout, RopeArgs& a) {
     if (rows > 0x7fffffffll / (head ? s.P : 1)) return ULYSSES_ERR_UNSUPPORTED;
     a.q.heads = head ? s.H / s.P : s.H;
     a.k.heads = head ? kv_info(s).Hkvp : hkv;
-    if (int64_t(a.q.heads) * s.d_h > (1 << 24)) return ULYSSES_ERR_UNSUPPORTED;
+    if (int64_t(a.q.heads) * s.d_h > kRopeMaxRow) return ULYSSES_ERR_UNSUPPORTED;
     a.d = s.d_h;
     a.rows = int(head ? rows * s.P : rows);
     a.seg = head ? s.L : s.L / s.P;
@@ -134,7 +137,7 @@ int ulysses_qk_rope_rows(int T, int H, int H_kv, int d_h, const ulysses_rope_t* 
     RopeArgs a{};
     int rc = rope_ok(rope, d_h);
     if (rc != ULYSSES_OK || (rc = norm_ok(w_q, w_k, w_fp32 != 0, eps)) != ULYSSES_OK) return rc;
-    if (int64_t(H) * d_h > (1 << 24) || int64_t(H_kv) * d_h > (1 << 24)) return ULYSSES_ERR_UNSUPPORTED;
+    if (int64_t(H) * d_h > kRopeMaxRow || int64_t(H_kv) * d_h > kRopeMaxRow) return ULYSSES_ERR_UNSUPPORTED;
     if (T == 0 || (!positions && B == 0)) return ULYSSES_OK;
     if (!q || !k || (!positions && (!cu_q || !kv_lens))) return ULYSSES_ERR_INVALID_ARG;
     const int64_t q_row = int64_t(H) * d_h, k_row = int64_t(H_kv) * d_h;

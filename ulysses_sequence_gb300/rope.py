@@ -97,6 +97,11 @@ def _weights(w_q, w_k, d: int, device: int, where: str):
     return w_q.data_ptr(), w_k.data_ptr(), int(w_q.dtype is _F32)
 
 
+def _like(x, device: int, stream):
+    """An output of x's shape and type, for the stream of the call."""
+    return torch.empty_like(x) if stream is None else _new(x.shape, _BF16, device, stream)
+
+
 def _same(x, name: str, shape, device: int, where: str) -> None:
     if not (x.shape == shape and x.dtype is _BF16 and x.get_device() == device and x.is_contiguous()):
         _refuse(x, name, shape, _BF16, device, where)
@@ -143,11 +148,11 @@ def qk_rope_fwd(q, k, P: int, rope: Rope, w_q=None, w_k=None, eps: float = 1e-6,
     wq, wk, wide = _weights(w_q, w_k, rope.d, dev, where)
     st = _stream_of(dev, stream, where)
     if q_out is None:
-        q_out = _new(q.shape, _BF16, dev, stream)
+        q_out = _like(q, dev, stream)
     else:
         _same(q_out, "q_out", q.shape, dev, where)
     if k_out is None:
-        k_out = _new(k.shape, _BF16, dev, stream)
+        k_out = _like(k, dev, stream)
     else:
         _same(k_out, "k_out", k.shape, dev, where)
     rc = U.load().ulysses_qk_rope_fwd(shape, layout, rope.ref, pos0, q.data_ptr(), k.data_ptr(), wq, wk, wide, eps,
@@ -169,11 +174,11 @@ def qk_rope_bwd(dq_out, dk_out, P: int, rope: Rope, q=None, k=None, w_q=None, w_
     wq, wk, wide = _weights(w_q, w_k, rope.d, dev, where)
     st = _stream_of(dev, stream, where)
     if dq is None:
-        dq = _new(dq_out.shape, _BF16, dev, stream)
+        dq = _like(dq_out, dev, stream)
     else:
         _same(dq, "dq", dq_out.shape, dev, where)
     if dk is None:
-        dk = _new(dk_out.shape, _BF16, dev, stream)
+        dk = _like(dk_out, dev, stream)
     else:
         _same(dk, "dk", dk_out.shape, dev, where)
     if wq is None:
