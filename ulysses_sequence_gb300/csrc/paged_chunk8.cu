@@ -3,14 +3,14 @@
 //
 // The products run in bf16: every key and value of such a cache, code x power of two, is exact in bf16, so nothing is
 // rounded that attention over a bf16 cache would not round, and queries stay as they are. Codes come into a small ring of
-// shared memory by bulk copies; four converter warps turn them into scaled bf16 (e4m3 pair -> fp16 pair -> two fp32, times
+// shared memory by bulk copies; six converter warps turn them into scaled bf16 (e4m3 pair -> fp16 pair -> two fp32, times
 // the scale -> bf16 pair) in the swizzled operand tiles. Warp roles (512 threads, a warpgroup each; registers are moved from
 // the first and the last to the two between):
 //   warp 0       producer: walks the share, looks up pages and scales (one lane to 16 keys), copies codes and queries, and
 //                publishes each piece and each tile;
 //   warp 1       MMA issuer;
 //   warps 4-7    softmax of tile 0, warps 8-11 of tile 1;
-//   warps 12-15  converters: 32 keys of every tile each. Values behind the request's last key become zeros (0 x NaN is NaN).
+//   warps 2, 3 and 12-15  converters: 32 keys or values of a tile in turn. Values behind the request's last key become zeros (0 x NaN is NaN).
 // A converter reads a row's 16 codes with one lane; eight lanes that read and write at once take four pieces of each of two
 // rows whose numbers differ in the bits that the swizzles of codes and of bf16 put on different banks.
 #define ULYSSES_SLOW_PATH __forceinline__
@@ -25,8 +25,9 @@ constexpr int kChunkRows = 2 * kTile;
 constexpr int kChunkMinCost = 4;     // the smallest share of a CTA, in key tiles
 constexpr int kChunkUnitCost = 3;    // the fixed cost of a unit, in key tiles
 // Registers of a thread by warpgroup: 512 threads are launched with 128 each.
-constexpr uint32_t kRegsIssue = 72, kRegsSoftmax = 176, kRegsConvert = 88;
-static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "no more than the launch brought");
+constexpr uint32_t kRegsSoftmax = 176, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * 128, "no more than the launch brought");
+constexpr int kConverters = 6;       // warps
 
 template <int D>
 struct Chunk8Cfg {
@@ -201,8 +202,8 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     volatile int* ab = abort_flag;
 
     // each warpgroup gives or takes its registers at the head of its branch, where the compiler counts them
-    if (warp < 4) {
-        regs_dec<kRegsIssue>();
+    if (warp < 4 || warp >= 12) {
+        regs_dec<kRegsOther>();
         if (warp == 0) {
             // ------------------------------------------------------------------ producer
             if (lane == 0) {
@@ -407,67 +408,63 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 umma_commit_one(one, drain);
                 mbar_drain(drain, 0);
             }
-        }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------------ converters
-        regs_dec<kRegsConvert>();
-        const int cw = warp - 12, quarter = lane >> 3;
-        // this lane's row within 8, and its 16 codes within 64
-        const int my_row = cw * 32 + (D == 128 ? ((lane & 4) ? quarter ^ 5 : quarter) : 2 * quarter + ((lane >> 2) & 1));
-        const int my_unit = lane & 3;
-        int nc = 0;
-        auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-            return __all_sync(0xffffffffu, chunk8_wait(bar, parity, ab, ROLE_LOAD, site));
-        };
-        // One tile of keys or values, in two halves of four units: the codes of a half first, so that no unit's loads stand
-        // behind another's stores, and a loop, because the roles' code together is more than the instruction cache likes (with
-        // a copy of this for tiles that reach the request's end: 1650 us, one for all without the loop: 1500 us).
-        auto convert = [&](uint8_t* tile, const float* by, int limit) {
-            const uint32_t codes = smem_u32(sC + (nc % C::NSC) * C::CODE_BYTES), out = smem_u32(tile);
+        } else {
+            // ------------------------------------------------------------------ converters
+            const int quarter = lane >> 3;
+            // this lane's row within 8, and its 16 codes within 64
+            const int my_row = D == 128 ? ((lane & 4) ? quarter ^ 5 : quarter) : 2 * quarter + ((lane >> 2) & 1);
+            const int my_unit = lane & 3;
+            auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+                return __all_sync(0xffffffffu, chunk8_wait(bar, parity, ab, ROLE_LOAD, site));
+            };
+            // 32 rows of a tile of keys or values, in two halves of four units: the codes of a half first, so that no unit's loads
+            // stand behind another's stores, and a loop, because the roles' code together is more than the instruction cache
+            // likes (8192 new tokens over 16384 keys: 1366 us; without the loop 1500 us; with a copy of it for tiles that reach
+            // the request's end 1650 us; loops of two units, one behind the other's loads, 1495 us).
+            auto convert = [&](uint8_t* tile, int stage, int part, const float* by, int limit) {
+                const uint32_t codes = smem_u32(sC + stage * C::CODE_BYTES), out = smem_u32(tile);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                uint4 x[2][D / 64];
+                for (int h = 0; h < 2; ++h) {
+                    uint4 x[2][D / 64];
 #pragma unroll
-                for (int g = 0; g < 2; ++g)  // 8 rows each
+                    for (int g = 0; g < 2; ++g)  // 8 rows each
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        x[g][c] = ld_shared_v4u(codes + code_offset<D>(my_row + 16 * h + 8 * g, 4 * c + my_unit));
-                const float s = by[cw * 2 + h];
+                        for (int c = 0; c < D / 64; ++c)
+                            x[g][c] = ld_shared_v4u(codes + code_offset<D>(32 * part + 16 * h + 8 * g + my_row, 4 * c + my_unit));
+                    const float s = by[part * 2 + h];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int row = my_row + 16 * h + 8 * g;
-                    const uint32_t a = out + row * 128, sw = row & 7;
+                    for (int g = 0; g < 2; ++g) {
+                        const int row = 32 * part + 16 * h + 8 * g + my_row;
+                        const uint32_t a = out + row * 128, sw = row & 7;
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        uint4 lo, hi;
-                        widen16(x[g][c], s, lo, hi);
-                        if (row >= limit) lo = hi = make_uint4(0, 0, 0, 0);
-                        st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit) ^ sw) << 4), lo.x, lo.y, lo.z, lo.w);
-                        st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit + 1) ^ sw) << 4), hi.x, hi.y, hi.z, hi.w);
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint4 lo, hi;
+                            widen16(x[g][c], s, lo, hi);
+                            if (row >= limit) lo = hi = make_uint4(0, 0, 0, 0);
+                            st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit) ^ sw) << 4), lo.x, lo.y, lo.z, lo.w);
+                            st_shared_v4(a + c * C::CHUNK_BYTES + (((2 * my_unit + 1) ^ sw) << 4), hi.x, hi.y, hi.z, hi.w);
+                        }
                     }
                 }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        for (int j = 0;; ++j) {
-            if (!wait(info_full + j % C::RING, (j / C::RING) & 1, 11)) break;
-            const ChunkTile* t = tile_info(j);
-            if (t->what & kInfoEnd) break;
-            bool ok = true;
-#pragma unroll 1
-            for (int value = 0; value < 2 && ok; ++value, ++nc) {
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            // a tile's keys and values are eight parts, dealt to the warps in turn
+            for (int x = warp < 4 ? warp - 2 : warp - 10;; x += kConverters) {
+                const int j = x >> 3, value = (x >> 2) & 1, part = x & 3, nc = 2 * j + value;
+                if (!wait(info_full + j % C::RING, (j / C::RING) & 1, 11)) break;
+                const ChunkTile* t = tile_info(j);
+                if (t->what & kInfoEnd) break;
                 const int ns = value ? NSV : NSK, st = j % ns;
                 uint64_t *full = (value ? v_full : k_full) + st, *empty = (value ? v_empty : k_empty) + st;
-                ok = wait(c_full + nc % C::NSC, (nc / C::NSC) & 1, 12) && (j < ns || wait(empty, ((j / ns) - 1) & 1, 13));
-                if (!ok) break;
-                convert((value ? sV : sK) + st * C::TILE_BYTES, value ? t->v : t->k, value ? t->limit : kTile);
+                if (!wait(c_full + nc % C::NSC, (nc / C::NSC) & 1, 12)) break;
+                if (j >= ns && !wait(empty, ((j / ns) - 1) & 1, 13)) break;
+                convert((value ? sV : sK) + st * C::TILE_BYTES, nc % C::NSC, part, value ? t->v : t->k, value ? t->limit : kTile);
                 if (lane == 0) {
                     mbar_arrive(full);
                     mbar_arrive(c_empty + nc % C::NSC);
                 }
             }
-            if (!ok) break;
         }
     } else {
         // ------------------------------------------------------------------ softmax (tile t)
