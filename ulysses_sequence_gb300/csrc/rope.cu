@@ -13,7 +13,8 @@
 // elements as two 16-byte pieces that are the two sides of its 8 pairs (or neighbours), so that pairs never leave the
 // lane and the norm is three (two) shuffles. The row's cosines and sines are computed once a row, D / 64 of them to a lane,
 // and handed round by shuffles. blockIdx.y names a part of the heads of q or k, so that weights and their
-// gradients stay in registers while a warp goes down its rows. Gradients of weights are summed in fp32 in a fixed order: by
+// gradients stay in registers while a warp goes down its rows. 32768 tokens of 32 + 8 heads of 128 with norms take 106 us
+// forward (6.4 TB/s, 0.94 of the measured copy bandwidth) and 169 us backward (6.0 TB/s). Gradients of weights are summed in fp32 in a fixed order: by
 // lane, by warp, by block into the workspace, and over the blocks by a second kernel, so they do not vary.
 #include <algorithm>
 
@@ -364,7 +365,9 @@ __global__ void __launch_bounds__(kRopeSumThreads) rope_dw_kernel(const float* p
 int passes(int heads, int d) { return (heads + 512 / d - 1) / (512 / d); }
 int chunks_of(int heads, int d, int U) { return (passes(heads, d) + U - 1) / U; }
 
-constexpr int kBwdPasses = 2;  // a warp's passes of a row in the backward kernel
+// A warp's passes of a row in the backward kernel (32768 tokens of 32 + 8 heads of 128: 175 us; with four, which spill, 186 us).
+// Two blocks to an SM: with three its 128 registers do not fit and it takes 255 us, more rows of blocks change nothing.
+constexpr int kBwdPasses = 2;
 
 template <int D, bool NORM, int U>
 int launch_fwd_t(const RopeParams& p, bool inter, dim3 grid, cudaStream_t stream) {
