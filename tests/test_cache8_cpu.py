@@ -1,11 +1,14 @@
 """CPU checks of the 8-bit cache calls: every refusal of the C ABI and of the torch helpers that needs no GPU, and pins of
 the oracle (e4m3 by hand and against torch, the append by hand)."""
 
+import re
+
 import numpy as np
 import pytest
 import torch
 
 import oracle.cache8 as cache8
+import test_kernel_sources_cpu as sources
 import ulysses_sequence_gb300 as U
 
 A, BIG = 1 << 20, 1 << 40  # addresses that are never dereferenced: each call is refused before a launch
@@ -132,3 +135,21 @@ def test_oracle_append_by_hand():
     # a smaller token changes no scale; rows outside the pool change nothing
     c2, s2 = cache8.append(c, s, x * 0 + 3.0, [5, -1, 32], 16)
     assert np.array_equal(s2, s) and cache8.TABLE[c2[0, 5, 0, 0]] == 3.0 and int((c2 != c).sum()) == 1
+
+
+# ------------------------------------------------------------------ the kernels' sources
+
+@pytest.mark.parametrize("name,waits", [("paged_decode8.cu", 1), ("paged_chunk8.cu", 3)])
+def test_kernels_wait_for_what_is_on_its_way(name, waits):
+    sources.test_kernels_wait_for_what_is_on_its_way_whatever_a_role_has_seen(name, waits)
+
+
+def test_chunk_warps_meet_before_instructions_for_whole_warps():
+    """Rows that leave the loop that stores them, and threads that loop over their own requests, meet before the next
+    tcgen05.ld and the allocation."""
+    text = sources.source("paged_chunk8.cu")
+    turn = text.index("if (!valid) continue;")
+    head = [m.end() for m in re.finditer(r"\bfor \([^{]*\{", text[:turn])][-1]
+    for at in (head, text.index("paged_costs<")):
+        before = text[at:at + re.search(sources.ALIGNED, text[at:]).start()]
+        assert sources.MEETS.search(before), before

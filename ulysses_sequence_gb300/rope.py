@@ -87,14 +87,25 @@ class Rope:
 
 def _weights(w_q, w_k, d: int, device: int, where: str):
     """(pointer, pointer, whether they are fp32) of the norms' weights."""
-    if w_q is None and w_k is None:
-        return None, None, 0
     if w_q is None or w_k is None:
-        raise ValueError(f"{where}: w_q and w_k must be given together")
-    for name, w in (("w_q", w_q), ("w_k", w_k)):
-        if not (w.shape == (d,) and w.dtype is w_q.dtype and w.dtype in (_BF16, _F32) and w.get_device() == device and w.is_contiguous()):
-            _refuse(w, name, (d,), w_q.dtype if w_q.dtype in (_BF16, _F32) else "bf16 or fp32", device, where)
-    return w_q.data_ptr(), w_k.data_ptr(), int(w_q.dtype is _F32)
+        if w_q is not w_k:
+            raise ValueError(f"{where}: w_q and w_k must be given together")
+        return None, None, 0
+    dtype, shape = w_q.dtype, (d,)
+    if dtype is not _BF16 and dtype is not _F32:
+        _refuse(w_q, "w_q", shape, "bf16 or fp32", device, where)
+    if not (w_q.shape == shape and w_q.get_device() == device and w_q.is_contiguous()):
+        _refuse(w_q, "w_q", shape, dtype, device, where)
+    if not (w_k.shape == shape and w_k.dtype is dtype and w_k.get_device() == device and w_k.is_contiguous()):
+        _refuse(w_k, "w_k", shape, dtype, device, where)
+    return w_q.data_ptr(), w_k.data_ptr(), int(dtype is _F32)
+
+
+def _rows(x, T: int, heads: int, d: int, device: int, name: str, where: str) -> int:
+    """_row_stride, with a short way for contiguous rows."""
+    if x.is_contiguous() and x.shape == (T, heads, d) and x.dtype is _BF16 and x.get_device() == device:
+        return heads * d
+    return _row_stride(x, T, heads, d, device, name, where)
 
 
 def _like(x, device: int, stream):
@@ -111,12 +122,17 @@ def _sharded(q, k, P: int, rope: Rope, layout: int, kv_heads: int, where: str) -
     """Shape of the sharded tensors of a call, checked."""
     if layout not in (U.LAYOUT_TOKEN_SHARDED, U.LAYOUT_HEAD_SHARDED):
         raise ValueError(f"{where}: layout must be LAYOUT_TOKEN_SHARDED or LAYOUT_HEAD_SHARDED, got {layout}")
-    if q.dim() != 5 or k.dim() != 5 or q.shape[0] != P or q.shape[:3] != k.shape[:3] or q.shape[4] != rope.d:
+    if q.dim() != 5 or k.dim() != 5:
         raise ValueError(f"{where}: q and k must be [{P}][B][tokens][heads][{rope.d}], got {tuple(q.shape)} and {tuple(k.shape)}")
-    _, B, tokens, heads, d = q.shape
-    kh = k.shape[3]
-    _same(q, "q", q.shape, rope.device, where)
-    _same(k, "k", (P, B, tokens, kh, d), rope.device, where)
+    groups, B, tokens, heads, d = q.shape
+    k_groups, k_B, k_tokens, kh, k_d = k.shape
+    if groups != P or d != rope.d or k_groups != P or k_B != B or k_tokens != tokens or k_d != d:
+        raise ValueError(f"{where}: q and k must be [{P}][B][tokens][heads][{rope.d}], got {tuple(q.shape)} and {tuple(k.shape)}")
+    dev = rope.device
+    if not (q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()):
+        _refuse(q, "q", q.shape, _BF16, dev, where)
+    if not (k.dtype is _BF16 and k.get_device() == dev and k.is_contiguous()):
+        _refuse(k, "k", k.shape, _BF16, dev, where)
     if layout == U.LAYOUT_TOKEN_SHARDED:
         if kv_heads not in (0, kh):
             raise ValueError(f"{where}: kv_heads is {kv_heads}, k has {kh}")
@@ -222,10 +238,12 @@ def qk_rope_rows(q, k, rope: Rope, positions=None, cu_q=None, kv_lens=None, w_q=
         raise ValueError(f"{where}: q and k must be [T][heads][{rope.d}], got {tuple(q.shape)} and {tuple(k.shape)}")
     T, H, d = q.shape
     H_kv = k.shape[1]
-    if max(T, H, H_kv) > _INT_MAX:
+    if T > _INT_MAX or H > _INT_MAX or H_kv > _INT_MAX:
         raise ValueError(f"{where}: rows and heads must fit 32 bits, got {T}, {H}, {H_kv}")
-    q_stride = _row_stride(q, T, H, rope.d, dev, "q", where)
-    k_stride = _row_stride(k, T, H_kv, rope.d, dev, "k", where)
+    if d != rope.d:
+        raise ValueError(f"{where}: q must be bf16 [{T}][{H}][{rope.d}], got {tuple(q.shape)}")
+    q_stride = _rows(q, T, H, d, dev, "q", where)
+    k_stride = _rows(k, T, H_kv, d, dev, "k", where)
     B = at = ends = lens = None
     if positions is not None:
         if cu_q is not None or kv_lens is not None:
@@ -246,12 +264,15 @@ def qk_rope_rows(q, k, rope: Rope, positions=None, cu_q=None, kv_lens=None, w_q=
         ends, lens = cu_q.data_ptr(), kv_lens.data_ptr()
     wq, wk, wide = _weights(w_q, w_k, d, dev, where)
     st = _stream_of(dev, stream, where)
+    q_out_stride, k_out_stride = H * d, H_kv * d
     if q_out is None:
         q_out = _new((T, H, d), _BF16, dev, stream)
+    else:
+        q_out_stride = q_stride if q_out is q else _rows(q_out, T, H, d, dev, "q_out", where)
     if k_out is None:
         k_out = _new((T, H_kv, d), _BF16, dev, stream)
-    q_out_stride = _row_stride(q_out, T, H, d, dev, "q_out", where)
-    k_out_stride = _row_stride(k_out, T, H_kv, d, dev, "k_out", where)
+    else:
+        k_out_stride = k_stride if k_out is k else _rows(k_out, T, H_kv, d, dev, "k_out", where)
     rc = U.load().ulysses_qk_rope_rows(T, H, H_kv, d, rope.ref, q.data_ptr(), q_stride, k.data_ptr(), k_stride, at, B, ends, lens,
                                        wq, wk, wide, eps, q_out.data_ptr(), q_out_stride, k_out.data_ptr(), k_out_stride, st)
     if rc:
