@@ -412,3 +412,63 @@ def test_serving_steps_with_norms_and_rotation():
         pools = [cache8.values(c, s, block) for c, s in zip(codes, scales)]
         ref = paged.paged_attention(q.double().cpu().numpy(), *pools, cu.cpu().numpy(), kv.cpu().numpy(), table.cpu().numpy(), True)
         hold(o, lse, ref, d)
+
+
+def test_one_step_captured_and_replayed_while_requests_grow():
+    """plan -> norm and rotation in place -> append -> attention in one graph, four steps replayed with nothing but lengths, rows
+    and the free list changed, each equal to the same calls made one by one on a copy of the state."""
+    H, Hkv, d, page, block, B, T = 8, 2, 64, 32, 16, 4, 6
+    rng = np.random.default_rng(3)
+    num, width, lens0 = 30, 8, [15, 31, 0, 40]
+    rope = U.Rope(d, rot=32, interleaved=True, scaling="linear", factor=2.0)
+    w = [torch.ones(d, device="cuda") for _ in range(2)]
+    table = np.full((B, width), -1)
+    order, at = rng.permutation(num), 0
+    for i, c in enumerate(lens0):
+        n = -(-c // page)
+        table[i, :n] = order[at:at + n]
+        at += n
+
+    def state():
+        cache = U.PagedCache8.empty(num, page, Hkv, d, block)
+        for t in (cache.k, cache.v):
+            t.view(torch.uint8).zero_()
+        s = dict(cache=cache, table=i32(table), cached=i32(lens0), free=i32(order[at:]), n_free=i32([num - at]),
+                 rows=torch.zeros(T, H + 2 * Hkv, d, dtype=torch.bfloat16, device="cuda"))
+        hist = torch.randn(2, sum(lens0), Hkv, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+        slots = [table[i, t // page] * page + t % page for i, c in enumerate(lens0) for t in range(c)]
+        U.kv_append(hist[0], hist[1], cache, i32(slots))
+        return s
+
+    def step(s):
+        q, k, v = s["rows"][:, :H], s["rows"][:, H:H + Hkv], s["rows"][:, H + Hkv:]
+        cu, kv, slots, info = U.page_plan(s["cached"], s["new"], s["free"], s["n_free"], s["table"], page, num, T)
+        U.qk_rope_rows(q, k, rope, cu_q=cu, kv_lens=kv, w_q=w[0], w_k=w[1], q_out=q, k_out=k)
+        U.kv_append(k, v, s["cache"], slots)
+        o, lse = U.paged_attn_fwd(q, s["cache"], cu, kv, s["table"], 2, workspace=s["ws"])
+        return kv, info, o, lse
+    a, b = state(), state()
+    for s in (a, b):
+        s["new"] = i32([1] * B)
+        s["ws"] = U.paged_attn_workspace(s["rows"][:, :H], s["cache"], 2)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        kv, info, o, lse = step(a)
+    for new in ([1, 1, 1, 1], [2, 1, 0, 1], [1, 1, 2, 1], [0, 1, 1, 2]):
+        x = bf16_rows(rng, T, H + 2 * Hkv, d).cuda()
+        for s in (a, b):
+            s["rows"].copy_(x)
+            s["new"].copy_(i32(new))
+        graph.replay()
+        want = step(b)
+        n = sum(new)
+        assert torch.equal(kv, want[0]) and torch.equal(info, want[1])
+        assert torch.equal(o[:n], want[2][:n]) and torch.equal(lse[:, :n], want[3][:, :n]) and torch.isfinite(o[:n]).all()
+        for p, q in zip((a["cache"].k, a["cache"].v, a["cache"].k_scale, a["cache"].v_scale),
+                        (b["cache"].k, b["cache"].v, b["cache"].k_scale, b["cache"].v_scale)):
+            assert np.array_equal(raw(p), raw(q))
+        for s in (a, b):
+            s["cached"].copy_(kv)
+            s["n_free"].sub_(info[1:2])
+    healthy()

@@ -322,3 +322,16 @@ def test_layer_forward_and_backward():
     # relative errors, and one more rounding of inputs and outputs
     for name, got, want in zip(("dq", "dk", "dv", "dw_q", "dw_k"), (dq, dk, dv, dwq, dwk), grads):
         assert rel(got, want) <= 1.5e-2, name
+
+
+def test_two_backward_calls_at_once():
+    """On two streams with workspaces of their own, the allocations and the sums apart."""
+    cases = [shard_case(2, 1, 4000, 16, 4, 128, 128, False, False, torch.bfloat16, 0, 1.0, seed=s) for s in (1, 2)]
+    want = [U.qk_rope_bwd(c[3], c[4], 2, c[0], c[1], c[2], *c[5], **c[6]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [U.qk_rope_bwd(c[3], c[4], 2, c[0], c[1], c[2], *c[5], stream=s, **c[6]) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(w, g))

@@ -7,6 +7,9 @@
 // - the batch has few units of few rows, at most three to two SMs: the chunk kernel then takes them along, which saves a
 //   launch and its fill (24 requests of 8 key/value heads, five of them chunks: 78 us against 83 us; 38: 114 us against
 //   111 us; 100 short ones, where its larger cost of a unit counts: 102 us against 90 us).
+//   Over an 8-bit cache, at most one to two SMs: the chunk kernel has codes to widen whatever a unit's rows (24 requests of 8
+//   key/value heads, some of them chunks: 97 us with both kernels, 104 us with one; 40 of 4 heads of 64: 44.7 us, 46.9 us; one
+//   chunk of 40 tokens over 1000 keys: 20.2 us, 17.4 us).
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -86,7 +89,7 @@ int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     const bool only = decode_only(p.G, a.max_q);
     PagedParts decode{}, chunk{};
     size_t bytes = 0;
-    const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > 3 * sms;
+    const bool both = decode_fits(p.G) && 2 * int64_t(p.B) * p.Hkv > (codes ? 1 : 3) * sms;
     p.min_rows = 1;
     if (only || both) {
         p.max_rows = only ? 0x7fffffff : paged_decode_rows();
