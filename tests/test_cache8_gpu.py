@@ -257,6 +257,17 @@ def test_scales_at_the_ends(n, shift):
     s.check(max_q=n)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_zero_keys_at_the_largest_scale(n):
+    """Queries of 2^100 and more against keys of zero: every score is zero, whatever the factors in front of it."""
+    s = Step8([(n, 300)], 4, 2, 64, 16, seed=n)
+    (kc, ks), v = s.parts
+    s.parts = [(np.zeros_like(kc), np.full_like(ks, 246)), v]
+    s.q = (s.q.double() * 2.0 ** 100).to(torch.bfloat16)
+    s.put()
+    s.check(max_q=n)
+
+
 def test_queries_of_very_different_elements():
     """Elements of a row down to 2^-24 of its largest, and rows of zeros."""
     s = Step8([(1, 200), (3, 90), (40, 100)], 8, 2, 128, 16, seed=5)

@@ -304,14 +304,15 @@ paged_decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             float sv[NG];  // log2 of the values' scales
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const float sk = t.scale[0][cw * NG + g];
+                // finite, also for the largest queries and scales: a zero score stays zero
+                const float sk = t.scale[0][cw * NG + g], k0 = fminf(sk * f0, 3e38f), k1 = fminf(sk * f1, 3e38f);
                 sv[g] = t.scale[1][cw * NG + g];
 #pragma unroll
                 for (int i = 2 * g; i < 2 * g + 2; ++i) {
-                    s[i][0] *= sk * f0;
-                    s[i][1] *= sk * f0;
-                    s[i][2] *= sk * f1;
-                    s[i][3] *= sk * f1;
+                    s[i][0] *= k0;
+                    s[i][1] *= k0;
+                    s[i][2] *= k1;
+                    s[i][3] *= k1;
                 }
             }
             const bool masked = flags & TILE_MASKED;
