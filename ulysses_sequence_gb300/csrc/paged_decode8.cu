@@ -15,9 +15,9 @@
 // log2 of the value scales, a row therefore holds two running maxima: m of s, for the sum of the weights, and n of s + v,
 // for O, whose weights are 2^(s + v - n + 7), at most 2^15: what contributes less than 2^-32 of the row's largest
 // contribution is dropped, whatever the scales. O goes back to the units of m at the end of a unit.
-// 64 requests of 64 to 8192 keys (32/8 heads of 128) take 108.5 us with the join, 5.1 TB/s of codes, 0.75 of the measured copy
+// 64 requests of 64 to 8192 keys (32/8 heads of 128) take 104 us with the join, 5.3 TB/s of codes, 0.79 of the measured copy
 // bandwidth (8191 keys each, twice the bytes: 179 us, 6.0 TB/s); leaving all products out changes 2%. One request of 1500 keys
-// takes 9.4 us, a chain of latencies.
+// takes 9.3 us, a chain of latencies.
 #include <algorithm>
 
 #include "paged_common.cuh"
