@@ -431,7 +431,7 @@ typedef struct {
  *   - code = x / scale to the nearest (ties to even); magnitudes past 448 * 2^119 and infinities become 448, NaN stays
  *     NaN and does not count for amax.
  * Tokens of one block must be consecutive rows of one call, as ulysses_page_plan places them: rows of one
- * block that are separated by another block's give undefined codes and scales in it. Slots should be distinct: where two
+ * block that are separated, by another block's or by skipped ones, give undefined codes and scales in it. Slots should be distinct: where two
  * rows name the same one, each 8-byte piece of it holds one or the other. Tokens whose slot lies outside the pool
  * are skipped. d_h: 64 or 128. */
 int ulysses_kv_append8(const ulysses_kv_cache8_t *cache, int T, const void *k, int64_t k_stride, const void *v,

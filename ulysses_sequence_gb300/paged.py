@@ -208,8 +208,8 @@ def kv_append(k, v, cache, slot_map, stream=None) -> None:
     """Writes the keys and values of new tokens, k, v bf16 [T][H_kv][d] (rows may be strided, as in a slice of a
     fused QKV product), to the slots slot_map[T] of the cache. Tokens with a slot outside the pool are skipped.
     Into a PagedCache8 they are rounded to codes, and the scales of their blocks are set (a block that begins with one
-    of them) or grown, its older tokens rounded again; rows of one block must then follow one another, as page_plan
-    places them."""
+    of them) or grown, its older tokens rounded again; rows of one block must then follow one another, without
+    skipped ones between them, as page_plan places them."""
     where, dev = "kv_append", cache.device
     T = k.shape[0] if k.dim() else 0
     if T > _INT_MAX:
