@@ -332,6 +332,24 @@ def test_chunks_equal_the_bf16_cache_of_the_same_values(n, d):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("reqs,H,Hkv,d", [([(2048, 6144)], 32, 8, 128), ([(2048, 6144)], 32, 8, 64), ([(300, 9000), (40, 4000), (700, 2500)], 8, 4, 128)])
+def test_long_chunks_equal_the_bf16_cache_many_times(reqs, H, Hkv, d):
+    """Shares of many key tiles, call after call, every other one with nothing in the L2, so that copies take different times: always
+    the bf16 cache's bits."""
+    s = Step8(reqs, H, Hkv, d, 64, 32, seed=d)
+    n = max(r[0] for r in reqs)
+    args = (i32(s.cu), i32(s.kv), i32(s.table), n)
+    k, v = (torch.nan_to_num(x).to(torch.bfloat16).cuda() for x in (s.k, s.v))
+    want = U.paged_attn_fwd(s.q, U.PagedCache(k, v), *args)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        if i % 2:
+            flush.fill_(i)
+        o, lse = U.paged_attn_fwd(s.q, s.cache, *args)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), i
+    healthy()
+
+
 @pytest.mark.parametrize("n", [1, 50])
 def test_same_bits_every_time(n):
     s = Step8([(n, c) for c in (3000, 10, 700)], 8, 2, 128, 16, seed=1)

@@ -51,7 +51,7 @@ struct Chunk8Cfg {
     static constexpr uint32_t OFF_INFO = OFF_PIECE + 128;
     static constexpr uint32_t OFF_SH = OFF_INFO + RING * 128;
     static constexpr uint32_t OFF_BAR = OFF_SH + 192;
-    static constexpr int BARS = 17 + 2 * (NSC + NSK + NSV) + RING;
+    static constexpr int BARS = 17 + 2 * (NSC + NSK + NSV) + 2 * RING;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + 640 + 1024;
     static_assert((kChunkThreads / 32 + 2) * 8 <= 192 && BARS * 8 + 8 <= 640, "room for the shares and the barriers");
     static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
@@ -65,6 +65,16 @@ struct Chunk8Cfg {
     // scores of tile n - NSC / 2 - NSK were done, and the softmax warps have read what describes the tile before that one
     // (with AHEAD the one before it).
     static_assert(NSC % 2 == 0 && NSC / 2 + NSK + (AHEAD ? 1 : 0) < RING, "tile descriptions outlive their readers");
+    // A wait by parity says that the phase is complete only where the phase before it is known to be: otherwise it passes on the
+    // one before that. The parts of a tile are dealt to the converter warps in turn, so a warp skips some tile's keys or
+    // values, and has not seen for itself that their codes landed. Before it waits for the codes of its own tile it
+    // therefore waits until the producer has found their stage free (info_full for keys, v_turn for values): the codes
+    // before them in the stage have then landed and been converted. Those two rings it may wait on because it meets every
+    // tile: of tile j - 1, which comes behind tile j - RING, it has seen one or the other.
+    static_assert(kConverters <= 8 && RING >= 2, "a converter warp takes at least one of a tile's eight parts");
+    // The same of the operand tiles: before it waits for the product of tile j - NS, that of tile j - 2 NS is known to be done, because
+    // the codes of tile j - NSC / 2 could only be converted behind the product of tile j - NSC / 2 - NS.
+    static_assert(NSC / 2 <= NSK && NSC / 2 <= NSV, "operand tiles are waited for one use at a time");
 };
 
 // One key tile.
@@ -150,7 +160,8 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint64_t* piece_full = o_done + 2;      // [2]
     uint64_t* piece_empty = piece_full + 2; // [2], MMA issuer and eight softmax warps
     uint64_t* info_full = piece_empty + 2;  // [RING]
-    uint64_t* c_full = info_full + C::RING;  // [NSC]
+    uint64_t* v_turn = info_full + C::RING;  // [RING], by tile: the stage of its values' codes is free
+    uint64_t* c_full = v_turn + C::RING;     // [NSC]
     uint64_t* c_empty = c_full + C::NSC;     // [NSC], the converter warps
     uint64_t* drain = c_empty + C::NSC;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -178,7 +189,10 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mbar_init(piece_full + t, 1);
             mbar_init(piece_empty + t, 9);
         }
-        for (int i = 0; i < C::RING; ++i) mbar_init(info_full + i, 1);
+        for (int i = 0; i < C::RING; ++i) {
+            mbar_init(info_full + i, 1);
+            mbar_init(v_turn + i, 1);
+        }
         for (int i = 0; i < C::NSC; ++i) {
             mbar_init(c_full + i, 1);
             mbar_init(c_empty + i, 4);
@@ -291,7 +305,6 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(info_full + n % C::RING);
-                    ++n;
                     copy(&tm_k, id, key0);
                     if (i == 0) {
                         // the unit's queries, once the previous piece's last scores are computed
@@ -308,6 +321,8 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         ++nq;
                     }
                     if (!(ok = room(4))) break;
+                    if (lane == 0) mbar_arrive(v_turn + n % C::RING);
+                    ++n;
                     copy(&tm_v, id, key0);
                     id = id_next;
                     byte = scale(id, key0 + kTile);
@@ -319,6 +334,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (ok && (ok = room(6)) && lane == 0) {
                 tile_info(n)->what = kInfoEnd;
                 mbar_arrive(info_full + n % C::RING);
+                mbar_arrive(v_turn + n % C::RING);
             }
             if (ok && (piece < 2 || (ok = wait(piece_empty + (piece & 1), ((piece >> 1) - 1) & 1, 5))) && lane == 0) {
                 pieces[piece & 1].tiles = 0;
@@ -458,7 +474,7 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             // a tile's keys and values are eight parts, dealt to the warps in turn
             for (int x = warp < 4 ? warp - 2 : warp - 10;; x += kConverters) {
                 const int j = x >> 3, value = (x >> 2) & 1, part = x & 3, nc = 2 * j + value;
-                if (!wait(info_full + j % C::RING, (j / C::RING) & 1, 11)) break;
+                if (!wait((value ? v_turn : info_full) + j % C::RING, (j / C::RING) & 1, 11)) break;
                 const ChunkTile* t = tile_info(j);
                 if (t->what & kInfoEnd) break;
                 const int ns = value ? NSV : NSK, st = j % ns;
