@@ -101,6 +101,16 @@ def test_shards_backward(case):
         check_bwd(got[i], got[2 + i] if normed else None, flat(dy), theta, r, flat(x), f64(ww) if normed else None, 1e-5, name, chain)
 
 
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (5, 5), (12, 3), (12, 4), (16, 8)])
+@pytest.mark.parametrize("d,inter", [(64, False), (128, True), (128, False)])
+def test_backward_without_epsilon(H, Hkv, d, inter):
+    """eps = 0, with numbers of heads that leave places of a warp without one: those add nothing to the weights' gradients."""
+    r, q, k, dq, dk, w, kw, theta = shard_case(2, 1, 21, H, Hkv, d, d, inter, False, torch.float32, 5, 1.0)
+    got = U.qk_rope_bwd(dq, dk, 2, r, q, k, *w, eps=0.0, **kw)
+    for i, (name, x, dy, ww) in enumerate((("dq", q, dq, w[0]), ("dk", k, dk, w[1]))):
+        check_bwd(got[i], got[2 + i], flat(dy), theta, r, flat(x), f64(ww), 0.0, name, 2 * (theta.shape[0] // 8 + 1) + 3 + 8 + 700)
+
+
 def test_backward_against_differences():
     """Central differences of the fp64 forward, along the GPU's own gradient: they must give its square."""
     r, q, k, dq, dk, w, kw, theta = shard_case(2, 1, 40, 8, 4, 64, 32, False, False, torch.float32, 7, 1.1)

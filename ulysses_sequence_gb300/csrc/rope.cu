@@ -296,13 +296,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeP
             unpack8(y[u][0], g);
             unpack8(y[u][1], g + 4);
             if (at.turned) rope_turn<INTER>(g, c, s);
-            const float r = inverse_rms<D>(x, p.eps);
+            // a head that is not there is zeros, and with eps = 0 its 1 / sqrt(0) would make NaN of them
+            const float rms = inverse_rms<D>(x, p.eps), r = h < t.heads ? rms : 0.f;
             const float2 rr = make_float2(r, r);
             float2 gx = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 x[i] = mul2(x[i], rr);
-                dw[i] = fma2(g[i], x[i], dw[i]);  // a head that is not there adds 0 * 0
+                dw[i] = fma2(g[i], x[i], dw[i]);  // a head that is not there adds 0
                 g[i] = mul2(g[i], w[i]);
                 gx = fma2(g[i], x[i], gx);
             }
