@@ -45,6 +45,16 @@ def test_fwd_refuses_bad_arguments(kw):
     assert fwd(**kw) == U.ERR_INVALID_ARG
 
 
+def test_one_tensor_as_queries_and_keys_is_not_written_in_place():
+    """Where q is k, a result over q would be read as keys."""
+    assert fwd(k=2 * A, qo=2 * A) == U.ERR_INVALID_ARG
+    assert fwd(k=2 * A, ko=2 * A) == U.ERR_INVALID_ARG
+    assert bwd(dko=2 * A, dq=2 * A) == U.ERR_INVALID_ARG
+    assert bwd(**dict(NORM, k=6 * A, dk=6 * A)) == U.ERR_INVALID_ARG
+    assert bwd(**dict(NORM, dko=6 * A, dq=6 * A)) == U.ERR_INVALID_ARG
+    assert rows(k=2 * A, qo=2 * A) == U.ERR_INVALID_ARG
+
+
 def test_fwd_refuses_no_rope():
     assert U.ulysses_qk_rope_fwd(U.Shape(*SHAPE), 0, None, 0, 2 * A, 3 * A, 0, 0, 0, 0.0, 4 * A, 5 * A, 0) == U.ERR_INVALID_ARG
 

@@ -57,8 +57,9 @@ int tensors_ok(const RopeArgs& a) {
             if (outs[i] && outs[i] == outs[j]) return ULYSSES_ERR_INVALID_ARG;
         for (const void* in : ins) {
             if (!outs[i] || outs[i] != in) continue;
-            const RopeTensors& t = i == 0 ? a.q : a.k;  // in place, element by element
+            const RopeTensors &t = i == 0 ? a.q : a.k, &other = i == 0 ? a.k : a.q;  // in place, element by element
             if (i > 1 || (in != t.x && in != t.dy) || t.x_stride != t.out_stride) return ULYSSES_ERR_INVALID_ARG;
+            if (in == other.x || in == other.dy) return ULYSSES_ERR_INVALID_ARG;  // blocks of the other side still read it
         }
     }
     const RopeTensors* sides[] = {&a.q, &a.k};
