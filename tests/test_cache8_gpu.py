@@ -112,6 +112,38 @@ def test_append_windows(T):
     run_append(codes, scales, rows, placed(rng, [(5, T)], page, pages), block)
 
 
+@pytest.mark.parametrize("H,d,page,block,head_major", [(8, 64, 64, 64, False), (5, 64, 256, 32, True), (3, 128, 64, 32, False), (4, 128, 256, 256, False),
+                                                       (1, 64, 4096, 256, False), (7, 128, 128, 128, True)])
+def test_append_of_many_rows_in_long_blocks(H, d, page, block, head_major):
+    """More than 1024 rows: prompts that begin and end anywhere, with blocks of one token and whole ones, single tokens, and rows of
+    no slot between and behind them, in runs that begin and end inside every window of rows."""
+    rng = np.random.default_rng(H + d + block)
+    lens = [(int(rng.integers(0, page)), int(rng.choice([1, 1, 1, 2, 7, 8, 9, 63, 64, 65, block - 1, block, block + 1]))) for _ in range(90)]
+    lens += [(block - 1, 700), (0, 2 * block), (5, 3 * block + 1)]
+    lens = [lens[i] for i in rng.permutation(len(lens))]
+    pages = sum((o + n - 1) // page + 1 for o, n in lens) + 2
+    parts, at = [], 0
+    for (_, n), gap in zip(lens, rng.integers(0, 4, len(lens))):
+        parts += [(at, n), (None, int(gap) * (gap > 1))]
+        at += n
+    flat = placed(rng, lens, page, pages)
+    slots = np.concatenate([flat[a:a + n] if a is not None else np.full(n, -1) for a, n in parts])
+    assert len(slots) > 1024 and (slots < 0).any()
+    codes, scales = pool(rng, pages, page, H, d, block)
+    rows = [bf16_rows(rng, len(slots), H, d) for _ in range(2)]
+    run_append(codes, scales, rows, slots, block, head_major, fused=H % 2 == 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_of_many_single_tokens_in_long_blocks(d):
+    """A step of 1500 requests with a token each, anywhere in blocks of 64."""
+    rng = np.random.default_rng(d)
+    T, H, page, block = 1500, 4, 64, 64
+    codes, scales = pool(rng, T + 5, page, H, d, block)
+    rows = [bf16_rows(rng, T, H, d) for _ in range(2)]
+    run_append(codes, scales, rows, rng.permutation(T + 5)[:T] * page + rng.integers(0, page, T), block)
+
+
 def test_append_of_extreme_values():
     """Zeros, the smallest and the largest bf16, infinities and NaN; magnitudes at and next to 448 * 2^n."""
     d = 64
