@@ -219,6 +219,21 @@ def test_rows(B, T, pad, H, Hkv, d, fused, wtype, far, given):
             check_fwd(y[T:], f64(x[T:]), theta_pad, r, None if ww is None else f64(ww), 1e-5, name)
 
 
+@pytest.mark.parametrize("d,wtype", [(64, None), (64, torch.bfloat16), (128, None), (128, torch.float32)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_many_rows_of_many_heads(d, wtype, inter):
+    """Rows enough for a warp to take several passes of one, two of them at a time, with heads left over; both layouts of pairs."""
+    T, H, Hkv = 4103, 37, 9
+    r = U.Rope(d, rot=d - 16, interleaved=inter, amplitude=1.1)
+    q, k = randn(d, T, H, d), randn(d + 1, T, Hkv, d)
+    w = weights(5, d, wtype) if wtype else [None, None]
+    at = np.random.default_rng(d).integers(0, 10 ** 6, T)
+    qo, ko = U.qk_rope_rows(q, k, r, positions=i32(at), w_q=w[0], w_k=w[1], eps=1e-5)
+    theta = rope.angles(at, r.frequencies)
+    for name, x, y, ww in (("q", q, qo, w[0]), ("k", k, ko, w[1])):
+        check_fwd(y, f64(x), theta, r, None if ww is None else f64(ww), 1e-5, name)
+
+
 def test_rows_in_place_in_fused_rows():
     r = U.Rope(128)
     rows = randn(3, 70, 14, 128)
