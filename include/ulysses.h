@@ -438,7 +438,9 @@ int ulysses_kv_append8(const ulysses_kv_cache8_t *cache, int T, const void *k, i
                        int64_t v_stride, const int32_t *slot_map, void *stream);
 
 /* ulysses_paged_attn_fwd over an 8-bit cache: the attention over the keys and values that the codes and scales stand
- * for; q, o and lse as there. Same arguments, limits, workspace (its size too) and rules. */
+ * for; q, o and lse as there. Same arguments, limits, workspace (its size too) and rules. Where a key/value head has at most
+ * 16 new rows, a key's softmax weight times its block's value scale may be rounded to 2^-11 of itself or to 2^-32 of
+ * the row's largest such product, whichever is more; otherwise weights are rounded to 2^-8 of themselves. */
 int ulysses_paged_attn8_fwd(const ulysses_kv_cache8_t *cache, int B, int T, int H, int max_q, int mask_kind, int window,
                             float softmax_scale, const void *q, int64_t q_stride, const int32_t *cu_q,
                             const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride, int max_pages,

@@ -300,6 +300,36 @@ def test_zero_keys_at_the_largest_scale(n):
     s.check(max_q=n)
 
 
+@pytest.mark.parametrize("d,shift", [(64, 6), (64, 20), (128, 30)])
+def test_heaviest_key_of_zeros_under_a_large_scale(d, shift):
+    """Decoding: the key with by far the largest weight has values of zero, in a block whose scale, 2^shift, its neighbours
+    have set. A key's weight times scale is held to 2^-11 of itself, and no finer than 2^-32 of the row's largest such product
+    (2^-25, half of fp16's smallest step, against 2^7); its codes go to 448. A score's d fp32 additions, 2^-24 of its magnitudes
+    each, count in the weight and in the sum."""
+    s = Step8([(1, 300)], 2, 1, d, 16, seed=shift, k_spread=0, v_spread=0)
+    t = 37
+    page = int(s.table[0, t // 16])
+    (kc, ks), (vc, vs) = s.parts
+    q = s.q[0].double().cpu().numpy()
+    kc[page, t % 16, 0] = np.where(q.sum(0) < 0, 0xfe, 0x7e)  # the largest code, towards the queries
+    vc[page, t % 16, 0] = 0
+    vs[page, 0, 0] += shift
+    s.put()
+    o, lse = s.run(1)
+    ref = s.oracle()
+    k, v = (x.double().numpy()[s.table[0, :-1]].reshape(-1, 1, d)[:s.kv[0], 0] for x in (s.k, s.v))
+    scores = q @ k.T / np.sqrt(d)
+    w = np.exp(scores - scores.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    assert (w.argmax(-1) == t).all()
+    by = np.repeat(2.0 ** (vs[s.table[0, :-1], 0, 0].astype(float) - 127), 16)[:s.kv[0]]
+    floor = 2.0 ** -32 * (w * by).max(-1, keepdims=True) * 448 * s.kv[0]
+    fp32 = 2 * 2.0 ** -24 * (d + 8) * (np.abs(q) @ np.abs(k).T).max() / np.sqrt(d)
+    off = np.abs(o[0].double().cpu().numpy() - ref["o"][0])
+    assert (off <= 2.0 ** -8 * np.abs(ref["o"][0]) + (2.0 ** -11 + fp32) * (w @ np.abs(v)) + floor).all()
+    assert np.isfinite(lse.cpu().numpy()).all()
+
+
 def test_queries_of_very_different_elements():
     """Elements of a row down to 2^-24 of its largest, and rows of zeros."""
     s = Step8([(1, 200), (3, 90), (40, 100)], 8, 2, 128, 16, seed=5)

@@ -13,8 +13,11 @@
 // 2^-28 of it stay exact. The keys' scales, powers of two by 16 keys at the finest, multiply the scores.
 // The values' scales belong to the weights, and fp16 has few exponents. With s the scores in the log2 domain and v the
 // log2 of the value scales, a row therefore holds two running maxima: m of s, for the sum of the weights, and n of s + v,
-// for O, whose weights are 2^(s + v - n + 7), at most 2^15: what contributes less than 2^-32 of the row's largest
-// contribution is dropped, whatever the scales. O goes back to the units of m at the end of a unit.
+// for O, whose weights are 2^(s + v - n + 7), at most 2^15 and for the heaviest key at least 2^7. fp16 keeps them to 2^-11 of
+// themselves, and to 2^-25 where they are small: 2^-32 of the row's largest weight times scale, whatever the scales. That
+// maximum does not know the codes, which span 2^18: where the heaviest key's codes are small or zero under a scale that its
+// neighbours set, a key of codes up to 448 may lose 448 * 2^-32 of that largest product, which can be more than 2^-32 of the
+// row's largest contribution. O goes back to the units of m at the end of a unit.
 // 64 requests of 64 to 8192 keys (32/8 heads of 128) take 104 us with the join, 5.3 TB/s of codes, 0.79 of the measured copy
 // bandwidth (8191 keys each, twice the bytes: 179 us, 6.0 TB/s); leaving all products out changes 2%. One request of 1500 keys
 // takes 9.3 us, a chain of latencies.
