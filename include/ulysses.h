@@ -274,8 +274,8 @@ int ulysses_usp_attn_bwd(ulysses_shape_t shape, int P_ring, const ulysses_mask_t
  *       (A (a cos theta - b sin theta), A (b cos theta + a sin theta)).
  * Pair e is (z_e, z_{e + rot/2}), or (z_2e, z_{2e+1}) when interleaved; elements from rot on pass
  * as they are. turns[rot/2] (device): f_e / (2 pi) in units of 2^-64 turns a token, modulo 2^64, so
- * angles are exact to 2^-31 turns at every position below 2^31; a scaling for long contexts is a
- * choice of f_e and A. rot: a multiple of 16, at most d_h (0: the norm alone). */
+ * angles are reduced to one turn to within 2^-32 turns at every position below 2^31, and then rounded to
+ * fp32 (off by up to 2^-26 turns); a scaling for long contexts is a choice of f_e and A. rot: a multiple of 16, at most d_h (0: the norm alone). */
 typedef struct {
     const uint64_t *turns;
     int rot;

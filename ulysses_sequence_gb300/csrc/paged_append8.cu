@@ -187,7 +187,10 @@ int launch_kv_append8(const ulysses_kv_cache8_t& c, int T, const void* k, int64_
     p.n_slots = c.num_pages * c.page_size;
     p.page_shift = __builtin_ctz(unsigned(c.page_size));
     p.block_shift = __builtin_ctz(unsigned(c.block));
-    // few rows are mostly single tokens: short groups, for the latency
+    // Few rows are mostly single tokens: short groups, for the latency. From 1025 rows on runs are taken to be long, which the
+    // host does not know: 32761 tokens of one prompt, 8 heads of 128 in blocks of 64, take 36.8 us shared by kParts groups, 52 us
+    // by groups of 16 rows, 56 us by those of four. Single tokens lose by it: 1500 of them take 50 us, 14.5 and 6.3 us, 6000 take
+    // 196, 49 and 20 us.
     const int groups = kThreads / (c.d_h / 8);
     const bool parts = c.block > 16 && T > 1024;
     const int y = (2 * c.H_kv * (parts ? kParts : 1) + groups - 1) / groups;

@@ -13,9 +13,9 @@
 //   warps 2, 3 and 12-15  converters: 32 keys or values of a tile in turn. Values behind the request's last key become zeros (0 x NaN is NaN).
 // A converter reads a row's 16 codes with one lane; eight lanes that read and write at once take four pieces of each of two
 // rows whose numbers differ in the bits that the swizzles of codes and of bf16 put on different banks.
-// 8192 new tokens over 16384 keys (32/8 heads of 128) take 1250 us, 1.32 PFLOP/s, 0.68 of the measured bf16 rate: the widening
-// beside the products bounds it (1094 us with codes stored as they are; the bf16 kernel 1050 to 1060 us). With four converter
-// warps 1349 us.
+// 8192 new tokens over 16384 keys (32/8 heads of 128) take 1252 us, 1.32 PFLOP/s, 0.68 of the measured bf16 rate: the widening
+// beside the products bounds it (1109 us with codes stored as they are; the bf16 kernel 1050 to 1060 us). With four converter
+// warps 1411 us. The same with heads of 64, half the work, takes 899 us: its softmax is the same.
 #define ULYSSES_SLOW_PATH __forceinline__
 #include "paged_common.cuh"
 
@@ -25,9 +25,9 @@ namespace {
 
 constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 2 * kTile;
-// The shares of the bf16 kernel, so that calls are cut alike and give its bits. The smallest, in key tiles: one chunk of 40 tokens
+// The shares of the bf16 kernel, so that calls of chunks are cut alike and give its bits. The smallest, in key tiles: one chunk of 40 tokens
 // over 1000 keys takes 17.4 us with 4 and would take 14.9 us with 2. The fixed cost of a unit, with 2, 3, 5: 24 mixed requests
-// 105.7, 104.4, 107.2 us, four chunks of 512 tokens 283, 286, 289 us.
+// 96.5, 97.3, 100.0 us, four chunks of 512 tokens 284, 286, 289 us.
 constexpr int kChunkMinCost = 4;
 constexpr int kChunkUnitCost = 3;
 // Registers of a thread by warpgroup: 512 threads are launched with 128 each.
@@ -441,8 +441,9 @@ paged_chunk8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             };
             // 32 rows of a tile of keys or values, in two halves of four units: the codes of a half first, so that no unit's loads
             // stand behind another's stores, and a loop, because the roles' code together is more than the instruction cache
-            // likes (8192 new tokens over 16384 keys: 1366 us; without the loop 1500 us; with a copy of it for tiles that reach
-            // the request's end 1650 us; loops of two units, one behind the other's loads, 1495 us).
+            // likes (8192 new tokens over 16384 keys, at the time with four converter warps: 1366 us; without the loop
+            // 1500 us; with a copy of it for tiles that reach the request's end 1650 us; loops of two units, one behind the
+            // other's loads, 1495 us).
             auto convert = [&](uint8_t* tile, int stage, int part, const float* by, int limit) {
                 const uint32_t codes = smem_u32(sC + stage * C::CODE_BYTES), out = smem_u32(tile);
 #pragma unroll 1

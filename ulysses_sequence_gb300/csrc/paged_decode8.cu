@@ -18,8 +18,8 @@
 // maximum does not know the codes, which span 2^18: where the heaviest key's codes are small or zero under a scale that its
 // neighbours set, a key of codes up to 448 may lose 448 * 2^-32 of that largest product, which can be more than 2^-32 of the
 // row's largest contribution. O goes back to the units of m at the end of a unit.
-// 64 requests of 64 to 8192 keys (32/8 heads of 128) take 104 us with the join, 5.3 TB/s of codes, 0.79 of the measured copy
-// bandwidth (8191 keys each, twice the bytes: 179 us, 6.0 TB/s); leaving all products out changes 2%. One request of 1500 keys
+// 64 requests of 64 to 8192 keys (32/8 heads of 128) take 104 to 109 us with the join, 5.1 to 5.3 TB/s of codes, 0.75 to 0.79 of
+// the measured copy bandwidth (8191 keys each, twice the bytes: 179 to 191 us, 5.6 to 6.0 TB/s); leaving all products out changes 2%. One request of 1500 keys
 // takes 9.3 us, a chain of latencies.
 #include <algorithm>
 

@@ -6,8 +6,9 @@
 //   backward  dz = R^T dy,  g = w dz,  r = 1 / sqrt(mean x^2 + eps),  dx = r (g - r x mean(g r x)),
 //             dw = sum over tokens and heads of dz r x.
 // Angles: f_e comes as turns a token in units of 2^-64, so that the product with the position, kept to 64 bits, is the
-// angle modulo one turn to 2^-34 turns at positions of 2^30, without a division or a 64-bit float; the upper 32 bits
-// go through sincospi.
+// angle modulo one turn to 2^-34 turns at positions below 2^31, without a division or a 64-bit float. Its upper 32 bits,
+// rounded to the 24 of fp32, go through sincospi: the angle used is off by up to 2^-26 turns (2^-23 radians), far below
+// the outputs' bf16.
 //
 // Bound by reading and writing the heads once. A warp takes a row's heads D / 16 lanes to a head: a lane holds 16
 // elements as two 16-byte pieces that are the two sides of its 8 pairs (or neighbours), so that pairs never leave the

@@ -34,7 +34,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = N
       "linear"  all divided by factor (positions interpolated);
       "ntk"     base grown by factor^(rot / (rot - 2)): the slowest pair is stretched by factor, the fastest not at all;
       "yarn"    by parts: with the turns r that a pair makes over `trained` tokens, frequencies of r >= high stay, those of
-                r <= low are divided by factor, linearly between; the amplitude is 0.1 ln(factor) + 1."""
+                r <= low are divided by factor, linearly in r between; the amplitude is 0.1 ln(factor) + 1. This is the formula
+                as published. Models have also been released with the ramp taken over the pair's number e between rounded
+                ends, which gives other frequencies: those go to Rope(frequencies=, amplitude=)."""
     if rot < 0 or rot % 2 != 0:
         raise ValueError(f"rope_frequencies: rot must be even and not negative, got {rot}")
     if not (base > 0 and factor >= 1 and trained > 0):
