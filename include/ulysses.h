@@ -286,7 +286,8 @@ typedef struct {
 /* The rotation (and norm) over a sharded layout, as ulysses_attn_fwd takes it: q, q_out with H heads, k,
  * k_out with H_kv (head-sharded: Hkvp) heads, bf16. Global token s has position pos0 + s. w_q, w_k
  * [d_h]: the norms' weights, fp32 when w_fp32 is nonzero, else bf16; both or neither (then eps is
- * not used). The norm and rotation are computed in fp32 and rounded once. q_out may be q and k_out may be k
+ * not used). The norm and rotation are computed in fp32 and rounded once; squares of a head's elements beyond
+ * 2^59 in magnitude overflow there, and with eps = 0 those of a head all below 2^-62 vanish. q_out may be q and k_out may be k
  * (in place), unless q and k are one tensor; outputs overlap no other tensor of the call.
  * TOKEN_SHARDED needs L % P == 0, but not H % P == 0 (the shards of the Ulysses-ring hybrid).
  * Supported: d_h in {64, 128}, fewer than 2^31 rows (B * L, head-sharded P * B * L), rows of up to 2^23
