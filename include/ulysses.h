@@ -299,7 +299,7 @@ int ulysses_qk_rope_fwd(ulysses_shape_t shape, int io_layout, const ulysses_rope
 /* Its gradient: dq_out, dk_out are those of q_out, k_out; dq, dk (bf16) those of q, k. With weights, q and
  * k are the forward's inputs (not needed without), and dw_q, dw_k [d_h] (fp32) are written: sums in fp32
  * over all tokens and heads in an order of their own, the same from run to run on one GPU model. dq may be dq_out
- * or q, dk may be dk_out or k. workspace (with weights): ulysses_qk_rope_bwd_workspace_size(shape) bytes,
+ * or q, dk may be dk_out or k, unless it is a tensor of both sides. workspace (with weights): ulysses_qk_rope_bwd_workspace_size(shape) bytes,
  * 16-byte aligned, contents need not be initialised; calls whose work overlaps need their own. With B == 0 or
  * L == 0, dw_q and dw_k are set to zero. */
 size_t ulysses_qk_rope_bwd_workspace_size(ulysses_shape_t shape);
